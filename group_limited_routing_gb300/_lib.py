@@ -26,6 +26,7 @@ MOE_STATUS_NONFINITE_LOGIT = 1
 MOE_STATUS_BAD_EXPERT_INDEX = 2
 MOE_STATUS_TIMEOUT = 4
 MOE_STATUS_COUNT_MISMATCH = 8
+MOE_STATUS_BAD_TARGET = 16
 
 MOE_WS_ROUTE = 0
 MOE_WS_FORWARD = 1
@@ -38,12 +39,15 @@ EXPORTS = ("moe_workspace_bytes", "moe_workspace_init", "moe_route", "moe_router
            "moe_debug_inject_timeout", "moe_rmsnorm", "moe_expert_feedback", "moe_prepare_router",
            "moe_route_prepared", "moe_dense_workspace_bytes", "moe_dense_ffn", "moe_backward",
            "moe_layer_workspace_bytes", "moe_layer", "moe_router_scores", "moe_ep_dispatch_workspace_bytes",
-           "moe_ep_dispatch", "moe_expert_rows_workspace_bytes", "moe_expert_rows", "moe_combine")
+           "moe_ep_dispatch", "moe_expert_rows_workspace_bytes", "moe_expert_rows", "moe_combine",
+           "moe_block_norm", "moe_block_norm_workspace_bytes", "moe_block_norm_backward",
+           "moe_vocab_loss_workspace_bytes", "moe_vocab_loss", "moe_vocab_loss_backward",
+           "moe_route_backward_workspace_bytes", "moe_route_backward")
 MOE_ROUTE_STATIC_SCRATCH_BYTES = 40 << 20
 MOE_LAYER_FUSED_ROUTER = 1
 MOE_LAYER_FUSED_COMBINE = 2
-MOE_KERNEL_COUNT = 19
-MOE_KERNEL_STAGE_ROUTE_PERMUTE = 18   # moe_profile_read id of the routing + bucketing stage (mode 2)
+MOE_KERNEL_COUNT = 30
+MOE_KERNEL_STAGE_ROUTE_PERMUTE = 29   # moe_profile_read id of the routing + bucketing stage (mode 2)
 
 
 class MoeCfg(ctypes.Structure):
@@ -132,6 +136,24 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.moe_combine.restype = ctypes.c_int
         lib.moe_router_scores.argtypes = [P, P, ctypes.c_int64, P]
         lib.moe_router_scores.restype = ctypes.c_int
+        F = ctypes.c_float
+        lib.moe_block_norm.argtypes = [I32, I32, I32, I32, P, P, P, P, P, F, F, P, P, P]
+        lib.moe_block_norm.restype = ctypes.c_int
+        lib.moe_block_norm_workspace_bytes.argtypes = [I32, I32, I32]
+        lib.moe_block_norm_workspace_bytes.restype = S
+        lib.moe_block_norm_backward.argtypes = [I32, I32, I32, I32, P, P, P, P, P, F, F] + [P] * 8 + [S, P]
+        lib.moe_block_norm_backward.restype = ctypes.c_int
+        I64 = ctypes.c_int64
+        lib.moe_vocab_loss_workspace_bytes.argtypes = [I32, I32, I32, ctypes.c_int]
+        lib.moe_vocab_loss_workspace_bytes.restype = S
+        lib.moe_vocab_loss.argtypes = [I32, I32, I32, P, P, P, I32, I64, P, P, P, S, P]
+        lib.moe_vocab_loss.restype = ctypes.c_int
+        lib.moe_vocab_loss_backward.argtypes = [I32, I32, I32, P, P, P, I32, I64, P, P, P, P, P, S, P]
+        lib.moe_vocab_loss_backward.restype = ctypes.c_int
+        lib.moe_route_backward_workspace_bytes.argtypes = [C]
+        lib.moe_route_backward_workspace_bytes.restype = S
+        lib.moe_route_backward.argtypes = [C] + [P] * 11 + [S, P]
+        lib.moe_route_backward.restype = ctypes.c_int
         lib.moe_strerror.argtypes = [ctypes.c_int]
         lib.moe_strerror.restype = ctypes.c_char_p
         for name in ("moe_workspace_init", "moe_route", "moe_router_logits", "moe_route_from_logits",

@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libglr_moe.so")
-SOURCES = ["api.cu", "route.cu", "permute.cu", "gemm.cu", "norm.cu"]
+SOURCES = ["api.cu", "api_train.cu", "route.cu", "permute.cu", "gemm.cu", "norm.cu", "block_norm.cu",
+           "pair_gemm.cu", "vocab.cu", "route_grad.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -15,32 +15,24 @@
 #include <mutex>
 #include <vector>
 
-#include "kernels.h"
-#include "moe.h"
+#include "host.h"
 
 using namespace glr;
+using namespace glr::host;
 
 namespace {
 
 thread_local int g_last_launches = 0;
 
 // ------------------------------------------------------------- profiling
-enum KernelId {
-    KID_SPLIT = 0, KID_ROUTER_GEMM, KID_SELECT, KID_FINALIZE, KID_HIST, KID_SCAN, KID_SCATTER,
-    KID_GEMM_GATE_UP, KID_GEMM_DOWN, KID_COMBINE, KID_DENSE_TILES, KID_BWD_RECOMPUTE, KID_BWD_DGRAD,
-    KID_BWD_DX, KID_BWD_WGRAD, KID_BWD_MISC, KID_ROUTE_FUSED, KID_TILES,
-    KID_STAGE_ROUTE_PERMUTE   // (per-stage timing) the routing and bucketing kernels as one interval
-};
 const char *const kKernelNames[MOE_KERNEL_COUNT] = {
     "split_router", "router_gemm", "route_select", "route_finalize", "bucket_hist",
     "bucket_scan", "bucket_scatter", "gemm_gate_up_swiglu", "gemm_down", "combine", "dense_tiles",
     "bwd_gate_up_recompute", "bwd_dgrad_down_swiglu", "bwd_dgrad_x", "bwd_weight_grads", "bwd_pad_and_dw",
-    "router_route_bucket", "bucket_tiles", "router_plus_permute"};
-
-struct ProfRecord {
-    cudaEvent_t start, stop;
-    int kid;
-};
+    "router_route_bucket", "bucket_tiles",
+    "block_norm", "block_norm_backward", "vocab_rows", "vocab_logits", "vocab_join", "vocab_dlogits",
+    "vocab_d_hidden", "vocab_d_weight", "route_backward_scores", "route_backward_d_hidden",
+    "route_backward_d_weight", "router_plus_permute"};
 
 std::atomic<int> g_prof_on{0};
 std::atomic<int> g_inject_timeouts{0};   // test-only: gate/up GEMM launches left to sabotage
@@ -93,58 +85,53 @@ void prof_close_stage_locked()
     t_stage = -1;
 }
 
-struct ProfScope {
-    bool on;
-    ProfRecord r;
-    cudaStream_t s;
-    ProfScope(int kid, cudaStream_t st) : on(g_prof_on.load(std::memory_order_relaxed) != 0), s(st)
-    {
-        if (!on)
-            return;
-        std::lock_guard<std::mutex> g(g_prof_mu);
-        if (g_prof_on.load(std::memory_order_relaxed) == 2) {
-            const int stage = prof_stage(kid);
-            if (stage != t_stage || st != t_stage_stream) {
-                prof_close_stage_locked();
-                t_stage = stage;
-                t_stage_stream = st;
-                t_stage_start = pool_event();
-                cudaEventRecord(t_stage_start, st);
-            }
-            on = false;
-            return;
+}  // namespace
+
+namespace glr {
+namespace host {
+
+void set_last_launches(int n) { g_last_launches = n; }
+
+ProfScope::ProfScope(int kid, cudaStream_t st) : on(g_prof_on.load(std::memory_order_relaxed) != 0), s(st)
+{
+    if (!on)
+        return;
+    std::lock_guard<std::mutex> g(g_prof_mu);
+    if (g_prof_on.load(std::memory_order_relaxed) == 2) {
+        const int stage = prof_stage(kid);
+        if (stage != t_stage || st != t_stage_stream) {
+            prof_close_stage_locked();
+            t_stage = stage;
+            t_stage_stream = st;
+            t_stage_start = pool_event();
+            cudaEventRecord(t_stage_start, st);
         }
-        r.start = pool_event();
-        r.stop = pool_event();
-        r.kid = kid;
-        cudaEventRecord(r.start, s);
-    }
-    void done()
-    {
-        if (!on)
-            return;
-        cudaEventRecord(r.stop, s);
-        std::lock_guard<std::mutex> g(g_prof_mu);
-        g_prof_pending.push_back(r);
         on = false;
+        return;
     }
-};
+    r.start = pool_event();
+    r.stop = pool_event();
+    r.kid = kid;
+    cudaEventRecord(r.start, s);
+}
 
-// At the end of every public call that launches kernels: closes the stage
-// left open by its last launch.
-struct ProfCall {
-    ~ProfCall()
-    {
-        if (g_prof_on.load(std::memory_order_relaxed) != 2)
-            return;
-        std::lock_guard<std::mutex> g(g_prof_mu);
-        prof_close_stage_locked();
-    }
-};
+void ProfScope::done()
+{
+    if (!on)
+        return;
+    cudaEventRecord(r.stop, s);
+    std::lock_guard<std::mutex> g(g_prof_mu);
+    g_prof_pending.push_back(r);
+    on = false;
+}
 
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+ProfCall::~ProfCall()
+{
+    if (g_prof_on.load(std::memory_order_relaxed) != 2)
+        return;
+    std::lock_guard<std::mutex> g(g_prof_mu);
+    prof_close_stage_locked();
+}
 
 // ------------------------------------------------------------- validation
 int check_route_cfg(const moe_cfg *c)
@@ -164,6 +151,11 @@ int check_route_cfg(const moe_cfg *c)
         return MOE_ERR_UNSUPPORTED_SHAPE;
     return MOE_OK;
 }
+
+}  // namespace host
+}  // namespace glr
+
+namespace {
 
 int check_forward_cfg(const moe_cfg *c)
 {
@@ -325,6 +317,11 @@ int check_backward_cfg(const moe_cfg *c)
     return MOE_OK;
 }
 
+}  // namespace
+
+namespace glr {
+namespace host {
+
 // --------------------------------------------------------------- device
 int device_check(int *sms)
 {
@@ -350,7 +347,7 @@ int device_check(int *sms)
     return MOE_OK;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
         void *p = nullptr;
@@ -364,40 +361,49 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-// 2D bf16 tensor [rows, cols] (row-major), box [box_rows, box_cols], 128-byte
-// swizzle (box_cols * 2 == 128), zero fill outside the tensor.
-bool make_map_bf16(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols, uint32_t box_cols,
-                   uint32_t box_rows)
+static bool make_map(CUtensorMap *m, CUtensorMapDataType type, uint32_t elem, const void *ptr, uint64_t rows,
+                     uint64_t cols, uint32_t box_cols, uint32_t box_rows)
 {
     auto fn = encode_fn();
     if (!fn)
         return false;
     cuuint64_t dims[2] = {cols, rows};
-    cuuint64_t strides[1] = {cols * 2};
+    cuuint64_t strides[1] = {cols * elem};
     cuuint32_t box[2] = {box_cols, box_rows};
     cuuint32_t estr[2] = {1, 1};
-    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    CUresult r = fn(m, type, 2, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
 
-WsHeader *header(void *ws) { return static_cast<WsHeader *>(ws); }
-
-template <typename T>
-T *at(void *ws, size_t off)
+bool make_map_bf16(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols, uint32_t box_cols,
+                   uint32_t box_rows)
 {
-    return reinterpret_cast<T *>(static_cast<char *>(ws) + off);
+    return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, rows, cols, box_cols, box_rows);
 }
 
-#define GLR_LAUNCH(kid, expr)                  \
-    do {                                       \
-        ProfScope prof_scope_((kid), s);       \
-        if ((expr) != cudaSuccess)             \
-            return MOE_ERR_CUDA;               \
-        prof_scope_.done();                    \
-        ++launches;                            \
-    } while (0)
+bool make_map_f32(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols, uint32_t box_cols,
+                  uint32_t box_rows)
+{
+    return make_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, ptr, rows, cols, box_cols, box_rows);
+}
+
+int check_ws(void *ws, size_t ws_bytes, size_t need)
+{
+    if (!ws)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(ws, 256))
+        return MOE_ERR_MISALIGNED;
+    if (ws_bytes < need)
+        return MOE_ERR_WORKSPACE_TOO_SMALL;
+    return MOE_OK;
+}
+
+}  // namespace host
+}  // namespace glr
+
+namespace {
 
 // counts (nullable) is cleared by the split kernel, for the routing kernel after it.
 // W_split: the bf16 x 3 split of W made by moe_prepare_router, or NULL to
@@ -541,17 +547,6 @@ int route_all(const moe_cfg &c, const moe_bf16 *hidden, const float *W, const mo
     if (counts_left)
         *counts_left = by_scan;
     return rc;
-}
-
-int check_ws(void *ws, size_t ws_bytes, size_t need)
-{
-    if (!ws)
-        return MOE_ERR_INVALID_ARG;
-    if (!aligned(ws, 256))
-        return MOE_ERR_MISALIGNED;
-    if (ws_bytes < need)
-        return MOE_ERR_WORKSPACE_TOO_SMALL;
-    return MOE_OK;
 }
 
 // ------------------------------------------------------------ moe_layer
@@ -836,8 +831,26 @@ int check_ep(const moe_cfg *c, int ranks)
     return MOE_OK;
 }
 
-
 }  // namespace
+
+namespace glr {
+namespace host {
+
+size_t route_region_bytes(const moe_cfg &c) { return route_layout(c).total; }
+
+uint16_t *route_region_split(const moe_cfg &c, void *ws) { return at<uint16_t>(ws, route_layout(c).w3); }
+
+int route_region_logits(const moe_cfg &c, const moe_bf16 *hidden, const float *W, const moe_bf16 *W_split, void *ws,
+                        int sms, cudaStream_t s, int &launches, float **logits)
+{
+    const RouteLayout L = route_layout(c);
+    int nparts = 1;
+    *logits = at<float>(ws, L.logits);
+    return router_gemm(c, hidden, W, W_split, *logits, nullptr, ws, L, sms, s, launches, 1, nparts);
+}
+
+}  // namespace host
+}  // namespace glr
 
 // ===================================================================== ABI
 extern "C" {

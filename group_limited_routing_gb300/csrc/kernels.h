@@ -114,6 +114,7 @@ constexpr int ST_NONFINITE = 1;
 constexpr int ST_BAD_INDEX = 2;
 constexpr int ST_TIMEOUT = 4;
 constexpr int ST_COUNT_MISMATCH = 8;
+constexpr int ST_BAD_TARGET = 16;
 
 // Workspace header (first 256 bytes of every workspace).
 struct WsHeader {
@@ -329,6 +330,108 @@ cudaError_t launch_dw_reduce(const int32_t *slot_of, const float *dw_part, int n
 
 cudaError_t launch_expert_feedback(const int32_t *counts, int E, int T, int k, float gamma, float *bias,
                                    long long *totals, cudaStream_t s);
+
+// ---- dense products of the training operators (pair_gemm.cu) ------------------
+// What the epilogue does with an accumulator tile (rows m, columns n):
+//   PG_STATS    the columns' softmax statistics per row, and the target's logit
+//   PG_DLOGITS  bf16( weight (exp(z - lse) - [n = target]) )
+//   PG_PARTIAL  fp32, stored or added to what is there (one slice per K split)
+//   PG_BF16     bf16( scale z (+ add) )
+enum PairEpilogue { PG_STATS = 0, PG_DLOGITS = 1, PG_PARTIAL = 2, PG_BF16 = 3 };
+
+// What the vocabulary operators' row kernel leaves for the kernels after it.
+struct VocabMeta {
+    int rows;      // rows that count (target in [0, V) and not ignored)
+    float scale;   // backward: largest |d_loss| of them (1 when that is not finite)
+};
+
+struct PairGemmParams {
+    CUtensorMap tmA, tmB, tmOut;
+    CUtensorMap tmHidden;     // the rows that count, packed: replaces A (STATS, DLOGITS) or B (BF16) when they are fewer than T
+    int T;                    // rows of `hidden`
+    const VocabMeta *meta;    // NULL: M and kblocks as given
+    int m_from_rows;          // M = meta->rows
+    int k_from_rows;          // K = meta->rows
+    int M, N;
+    int nseg, kblocks;        // K = nseg segments of kblocks blocks of 64
+    int a_off[3], b_off[3];   // per segment: rows added to the operand's row coordinate
+    int splits;               // K range cut into this many parts (inside every segment)
+    int group_m;              // tiles run m-fastest within groups of this many m-tiles
+    int out_row0;             // row of the output map where row 0 goes
+    int out_rows, out_cols;   // the output map's extent
+    int split_rows;           // PG_PARTIAL: rows between the splits' slices
+    int accumulate;           // PG_PARTIAL: add to the slice
+    // PG_STATS, PG_DLOGITS
+    const int *target;        // per packed row
+    int n0;                   // vocabulary id of column 0
+    float2 *stats;            // [n-tiles][ld_stats] (base of the exponentials in log2, their sum)
+    int ld_stats;
+    float *target_logit;      // per packed row
+    const float *lse, *weight; // per packed row
+    // PG_BF16
+    const uint16_t *add;      // [out_rows, N] or NULL
+    int *status;
+};
+cudaError_t launch_pair_gemm(PairEpilogue epi, bool a_mn, bool b_mn, const PairGemmParams &p, int max_units,
+                             cudaStream_t s);
+
+// ---- vocabulary loss (vocab.cu) -----------------------------------------------
+struct VocabRowsParams {
+    int T, V, target_bits;
+    const void *target;
+    long long ignore;
+    VocabMeta *meta;
+    int *row_of;              // packed row -> row
+    int *packed_target;
+    int *status;
+    float *loss, *lse_out;    // forward: zeroed where a row does not count
+    // backward
+    int *packed_of;           // row -> packed row, or -1
+    const float *lse, *d_loss;
+    float *packed_lse, *packed_weight;
+};
+cudaError_t launch_vocab_rows(const VocabRowsParams &p, cudaStream_t s);
+cudaError_t launch_vocab_pack(const uint16_t *hidden, const VocabMeta *meta, const int *row_of, int T, int H,
+                              uint16_t *packed, cudaStream_t s);
+cudaError_t launch_vocab_join(const float2 *stats, int ntiles, int ld, const float *target_logit,
+                              const VocabMeta *meta, const int *row_of, int T, float *loss, float *lse,
+                              cudaStream_t s);
+cudaError_t launch_vocab_dx_join(const float *part, int splits, long long split_stride, const VocabMeta *meta,
+                                 const int *packed_of, int T, int H, uint16_t *d_hidden, cudaStream_t s);
+
+// ---- the router's gradient (route_grad.cu) --------------------------------------
+cudaError_t launch_route_grad(const float *logits, const int32_t *idx, const float *d_w, const int32_t *counts,
+                              const float *d_aux, int T, int E, int k, float rsf, float eps, uint16_t *parts,
+                              int *status, cudaStream_t s);
+// out[i] = sum over the splits of part[s stride + i], i < n
+cudaError_t launch_sum_splits(const float *part, int splits, long long stride, long long n, float *out,
+                              cudaStream_t s);
+
+// ---- norms around a block (block_norm.cu) ------------------------------------
+struct BlockNormParams {
+    int T, H;
+    int groups, rows_per_gate;       // gate rows, T / groups
+    int cpg;                         // backward: chunks per gate row
+    float alpha, eps;
+    const void *x;                   // [T, H] bf16 or fp32 (the stream's type)
+    const uint16_t *y;               // [T, H] bf16, or NULL
+    const float *gate;               // [groups, H] or NULL (1)
+    const float *w_post, *w_pre;     // [H] or NULL (1)
+    void *r;                         // [T, H], the stream's type, or NULL
+    uint16_t *n;                     // [T, H] bf16
+    const void *d_r;                 // [T, H], the stream's type, or NULL (0)
+    const uint16_t *d_n;             // [T, H] bf16
+    void *d_x;                       // [T, H], the stream's type
+    uint16_t *d_y;                   // [T, H] bf16
+    float *part_a, *part_b;          // partial column sums [groups cpg, H] (NULL without y), [blocks, H]
+    float *d_gate, *dw_post, *dw_pre; // each may be NULL
+};
+constexpr int BLOCK_NORM_MAX_H = 8192;   // a row is one block's registers
+int block_norm_blocks(int T, int H, int sms);
+int block_norm_cpg(int T, int groups, int blocks);
+cudaError_t launch_block_norm(const BlockNormParams &p, bool stream_f32, int blocks, cudaStream_t s);
+cudaError_t launch_block_norm_backward(const BlockNormParams &p, bool stream_f32, int blocks, cudaStream_t s);
+cudaError_t launch_block_norm_finish(const BlockNormParams &p, int blocks, cudaStream_t s);
 
 cudaError_t launch_rmsnorm(const uint16_t *x, uint16_t *out, int T, int H, float eps, cudaStream_t s);
 

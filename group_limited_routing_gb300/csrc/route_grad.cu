@@ -1,0 +1,172 @@
+// The router's gradient: from the gradient of the routing weights (and of the
+// balance loss) to that of the logits, in the form the tensor-core products
+// of pair_gemm.cu read.
+//
+// With s = sigmoid(L), S the chosen experts of a token and D = sum_S s + eps,
+// w_j = rsf s_j / D, so  ds_j = rsf / D (dw_j - sum_i dw_i s_i / D).  The balance
+// loss E sum_e f_e mean_t(s_te / Z_t), Z_t = sum_e s_te, f_e = counts_e / (k T)
+// fixed, adds  ds_e += d_aux E / T (f_e - sum_e' f_e' s_e' / Z) / Z.  Then
+// dL = ds s (1 - s), with 1 - s as sigmoid(-L), which keeps its digits near s = 1.
+//
+// dL is written as three bf16 parts (high, middle, low: 24 bits, as the router
+// weight is split for the forward), so that the products with the bf16 hidden
+// rows are exact and the gradient of the fp32 router weight keeps fp32 accuracy.
+#include <cuda_bf16.h>
+
+#include "kernels.h"
+
+namespace glr {
+
+namespace {
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+__device__ __forceinline__ uint16_t bf16_bits(float v)
+{
+    const __nv_bfloat16 b = __float2bfloat16_rn(v);
+    return *reinterpret_cast<const uint16_t *>(&b);
+}
+
+}  // namespace
+
+// One warp per token; a lane holds EPL = E / 32 neighbouring experts.
+template <int EPL>
+__global__ void __launch_bounds__(256) route_grad_kernel(const float *__restrict__ logits,
+                                                         const int32_t *__restrict__ idx,
+                                                         const float *__restrict__ d_w,
+                                                         const int32_t *__restrict__ counts,
+                                                         const float *__restrict__ d_aux, int T, int k, float rsf,
+                                                         float eps, uint16_t *parts, int *status)
+{
+    constexpr int E = EPL * 32;
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int warps = gridDim.x * (blockDim.x >> 5);
+    float f[EPL];
+    const float aux = d_aux ? *d_aux * ((float)E / (float)T) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+        f[i] = d_aux ? (float)counts[lane * EPL + i] / ((float)k * (float)T) : 0.0f;
+    for (int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); t < T; t += warps) {
+        const float *row = logits + (size_t)t * E;
+        float L[EPL], ds[EPL], s[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; i += 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(row + lane * EPL + i);
+            L[i] = q.x; L[i + 1] = q.y; L[i + 2] = q.z; L[i + 3] = q.w;
+        }
+        // lane j < k: the chosen expert j
+        int e = -1;
+        float dw = 0.0f, sj = 0.0f;
+        if (lane < k) {
+            e = idx[(size_t)t * k + lane];
+            if (e < 0 || e >= E) {
+                atomicOr(status, ST_BAD_INDEX);
+                e = -1;
+            } else {
+                dw = d_w[(size_t)t * k + lane];
+                sj = router_sigmoid(row[e]);
+            }
+        }
+        const float D = warp_sum(sj) + eps;
+        const float dot = warp_sum(dw * sj);
+        const float dsj = rsf / D * (dw - dot / D);
+        bool finite = true;
+        float Z = 0.0f, F = 0.0f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            finite &= fabsf(L[i]) < INFINITY;
+            s[i] = router_sigmoid(L[i]);
+            Z += s[i];
+            F = fmaf(f[i], s[i], F);
+            ds[i] = 0.0f;
+        }
+        if (!__all_sync(0xffffffffu, finite) && lane == 0)
+            atomicOr(status, ST_NONFINITE);
+        for (int j = 0; j < k; ++j) {
+            const int ej = __shfl_sync(0xffffffffu, e, j);
+            const float v = __shfl_sync(0xffffffffu, dsj, j);
+            const int at = ej - lane * EPL;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if (ej >= 0 && at == i)
+                    ds[i] += v;
+        }
+        if (d_aux) {
+            Z = warp_sum(Z);
+            F = warp_sum(F);
+            const float c = aux / Z, m = F / Z;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                ds[i] = fmaf(c, f[i] - m, ds[i]);
+        }
+        uint16_t h[3][EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            float v = ds[i] * s[i] * router_sigmoid(-L[i]);
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+                h[q][i] = bf16_bits(v);
+                v -= __uint_as_float((uint32_t)h[q][i] << 16);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+            uint32_t o[EPL / 2];
+#pragma unroll
+            for (int i = 0; i < EPL / 2; ++i)
+                o[i] = (uint32_t)h[q][2 * i] | ((uint32_t)h[q][2 * i + 1] << 16);
+            uint16_t *dst = parts + ((size_t)q * T + t) * E + lane * EPL;
+            if constexpr (EPL == 8)
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+            else
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(o[0], o[1]);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(256) sum_splits_kernel(const float *__restrict__ part, int splits, long long stride,
+                                                         long long n4, float *out)
+{
+    pdl_wait();
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= n4)
+        return;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int s = 0; s < splits; ++s) {
+        const float4 q = __ldcs(reinterpret_cast<const float4 *>(part + s * stride) + i);
+        a.x += q.x; a.y += q.y; a.z += q.z; a.w += q.w;
+    }
+    reinterpret_cast<float4 *>(out)[i] = a;
+}
+
+cudaError_t launch_route_grad(const float *logits, const int32_t *idx, const float *d_w, const int32_t *counts,
+                              const float *d_aux, int T, int E, int k, float rsf, float eps, uint16_t *parts,
+                              int *status, cudaStream_t s)
+{
+    const int want = (T + 7) / 8, most = 152 * 8;
+    const dim3 grid(want < most ? want : most);
+    const cudaError_t e = E == 256 ? launch_pdl(route_grad_kernel<8>, grid, dim3(256), 0, s, logits, idx, d_w, counts,
+                                                d_aux, T, k, rsf, eps, parts, status)
+                                   : launch_pdl(route_grad_kernel<4>, grid, dim3(256), 0, s, logits, idx, d_w, counts,
+                                                d_aux, T, k, rsf, eps, parts, status);
+    return e != cudaSuccess ? e : cudaPeekAtLastError();
+}
+
+cudaError_t launch_sum_splits(const float *part, int splits, long long stride, long long n, float *out,
+                              cudaStream_t s)
+{
+    const long long n4 = n / 4;
+    const cudaError_t e = launch_pdl(sum_splits_kernel, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, s, part,
+                                     splits, stride, n4, out);
+    return e != cudaSuccess ? e : cudaPeekAtLastError();
+}
+
+}  // namespace glr

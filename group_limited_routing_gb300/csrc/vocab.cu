@@ -1,0 +1,225 @@
+// Vocabulary loss: the kernels around the dense products of pair_gemm.cu.
+//
+//   z[t, v] = <hidden_t, W_v>,  lse_t = log sum_v exp z[t, v],
+//   loss_t = lse_t - z[t, target_t]
+//
+// The products run over the rows that count only (a target in [0, V) that is
+// not the ignored one): their row numbers are packed here, and their hidden
+// rows too where some row does not count, so that masked rows (prompts,
+// padding) cost nothing and a NaN in one reaches no gradient.  All of these
+// kernels move a few percent of the products' bytes; they are bound by launch
+// and memory latency.
+#include <cuda_bf16.h>
+
+#include "kernels.h"
+
+namespace glr {
+
+namespace {
+
+__device__ __forceinline__ long long target_at(const VocabRowsParams &p, int t)
+{
+    return p.target_bits == 64 ? static_cast<const long long *>(p.target)[t]
+                               : (long long)static_cast<const int *>(p.target)[t];
+}
+
+constexpr int ROWS_THREADS = 1024;
+
+}  // namespace
+
+// One block: thread i counts the rows of its run of rows, a scan over the
+// threads gives each its first packed row.
+__global__ void __launch_bounds__(ROWS_THREADS) vocab_rows_kernel(const VocabRowsParams p)
+{
+    __shared__ int warp_sum[32];
+    __shared__ float warp_max[32];
+    pdl_wait();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int per = (p.T + ROWS_THREADS - 1) / ROWS_THREADS;
+    const int t0 = min(p.T, (int)threadIdx.x * per), t1 = min(p.T, t0 + per);
+    int n = 0;
+    bool bad = false;
+    float top = 0.0f;
+    for (int t = t0; t < t1; ++t) {
+        const long long v = target_at(p, t);
+        const bool counts = v != p.ignore && v >= 0 && v < p.V;
+        bad |= !counts && v != p.ignore;
+        n += counts;
+        if (p.d_loss && counts) {
+            const float g = fabsf(p.d_loss[t]);
+            top = g > top || g != g ? g : top;      // a NaN stays
+        }
+    }
+    if (bad)
+        atomicOr(p.status, ST_BAD_TARGET);
+    int at = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, at, off);
+        if (lane >= off)
+            at += o;
+        const float f = __shfl_xor_sync(0xffffffffu, top, off);
+        top = f > top || f != f ? f : top;
+    }
+    if (lane == 31)
+        warp_sum[w] = at;
+    if (lane == 0)
+        warp_max[w] = top;
+    __syncthreads();
+    int before = 0, total = 0;
+    top = 0.0f;
+    for (int i = 0; i < 32; ++i) {
+        if (i < w)
+            before += warp_sum[i];
+        total += warp_sum[i];
+        top = warp_max[i] > top || warp_max[i] != warp_max[i] ? warp_max[i] : top;
+    }
+    const float scale = top > 0.0f && top < INFINITY ? top : 1.0f;
+    if (threadIdx.x == 0) {
+        p.meta->rows = total;
+        p.meta->scale = scale;
+    }
+    int r = before + at - n;
+    for (int t = t0; t < t1; ++t) {
+        const long long v = target_at(p, t);
+        const bool counts = v != p.ignore && v >= 0 && v < p.V;
+        if (p.packed_of)
+            p.packed_of[t] = counts ? r : -1;
+        if (counts) {
+            p.row_of[r] = t;
+            p.packed_target[r] = (int)v;
+            if (p.d_loss) {
+                p.packed_lse[r] = p.lse[t];
+                p.packed_weight[r] = p.d_loss[t] / scale;
+            }
+            ++r;
+        } else if (p.loss) {
+            p.loss[t] = 0.0f;
+            p.lse_out[t] = 0.0f;
+        }
+    }
+}
+
+// The counting rows' hidden states side by side, then zero rows up to a
+// multiple of 64 (a K block of the weight gradient).  Nothing to do when every
+// row counts: the products then read `hidden` itself.
+__global__ void __launch_bounds__(128) vocab_pack_kernel(const uint16_t *__restrict__ hidden, const VocabMeta *meta,
+                                                         const int *row_of, int T, int H, uint16_t *packed)
+{
+    pdl_wait();
+    const int rows = meta->rows;
+    if (rows == T)
+        return;
+    const int padded = min(T, (rows + 63) / 64 * 64);
+    const int nv = H / 8;
+    for (int r = blockIdx.x; r < padded; r += gridDim.x) {
+        const uint4 *src = r < rows ? reinterpret_cast<const uint4 *>(hidden) + (size_t)row_of[r] * nv : nullptr;
+        uint4 *dst = reinterpret_cast<uint4 *>(packed) + (size_t)r * nv;
+        for (int v = threadIdx.x; v < nv; v += blockDim.x)
+            dst[v] = src ? src[v] : make_uint4(0, 0, 0, 0);
+    }
+}
+
+// Joins the tiles' softmax statistics of each row: lane = row, 32 warps share
+// the tiles.  The bases are log2 values, so the sums are over powers of two.
+__global__ void __launch_bounds__(1024) vocab_join_kernel(const float2 *__restrict__ stats, int ntiles, int ld,
+                                                          const float *__restrict__ target_logit,
+                                                          const VocabMeta *meta, const int *row_of, float *loss,
+                                                          float *lse)
+{
+    __shared__ float2 sm[32][33];
+    pdl_wait();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int row = blockIdx.x * 32 + lane;
+    const bool in = row < meta->rows;
+    float b = -INFINITY, s = 0.0f;
+    auto join = [&](float b2, float s2) {
+        const float top = fmaxf(b, b2);
+        if (top > -INFINITY) {
+            s = s * exp2f(b - top) + s2 * exp2f(b2 - top);
+            b = top;
+        }
+    };
+#pragma unroll 4
+    for (int i = w; i < ntiles; i += 32)
+        if (in) {
+            const float2 v = stats[(size_t)i * ld + row];
+            join(v.x, v.y);
+        }
+    sm[w][lane] = make_float2(b, s);
+    __syncthreads();
+    if (w != 0 || !in)
+        return;
+    for (int i = 1; i < 32; ++i)
+        join(sm[i][lane].x, sm[i][lane].y);
+    const float l = (b + log2f(s)) * 0.69314718055994531f;
+    const int t = row_of[row];
+    lse[t] = l;
+    loss[t] = l - target_logit[row];
+}
+
+// d_hidden[t] = bf16( scale sum_s part[s][packed row of t] ), zero where the
+// row does not count.  Splits in order.
+__global__ void __launch_bounds__(128) vocab_dx_join_kernel(const float *__restrict__ part, int splits,
+                                                            long long split_stride, const VocabMeta *meta,
+                                                            const int *packed_of, int T, int H, uint16_t *d_hidden)
+{
+    pdl_wait();
+    const float scale = meta->scale;
+    const int nv = H / 8;
+    for (int t = blockIdx.x; t < T; t += gridDim.x) {
+        const int r = packed_of[t];
+        for (int v = threadIdx.x; v < nv; v += blockDim.x) {
+            float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (r >= 0)
+                for (int s = 0; s < splits; ++s) {
+                    const float4 *q = reinterpret_cast<const float4 *>(part + s * split_stride + (size_t)r * H) + 2 * v;
+                    const float4 a = __ldcs(q), b = __ldcs(q + 1);
+                    f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
+                    f[4] += b.x; f[5] += b.y; f[6] += b.z; f[7] += b.w;
+                }
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i] * scale, f[2 * i + 1] * scale);
+                o[i] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            reinterpret_cast<uint4 *>(d_hidden)[(size_t)t * nv + v] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+}
+
+cudaError_t launch_vocab_rows(const VocabRowsParams &p, cudaStream_t s)
+{
+    const cudaError_t e = launch_pdl(vocab_rows_kernel, dim3(1), dim3(ROWS_THREADS), 0, s, p);
+    return e != cudaSuccess ? e : cudaPeekAtLastError();
+}
+
+cudaError_t launch_vocab_pack(const uint16_t *hidden, const VocabMeta *meta, const int *row_of, int T, int H,
+                              uint16_t *packed, cudaStream_t s)
+{
+    const int blocks = T < 2432 ? T : 2432;      // 152 SMs x 16
+    const cudaError_t e = launch_pdl(vocab_pack_kernel, dim3(blocks), dim3(128), 0, s, hidden, meta, row_of, T, H,
+                                     packed);
+    return e != cudaSuccess ? e : cudaPeekAtLastError();
+}
+
+cudaError_t launch_vocab_join(const float2 *stats, int ntiles, int ld, const float *target_logit,
+                              const VocabMeta *meta, const int *row_of, int T, float *loss, float *lse,
+                              cudaStream_t s)
+{
+    const cudaError_t e = launch_pdl(vocab_join_kernel, dim3((T + 31) / 32), dim3(1024), 0, s, stats, ntiles, ld,
+                                     target_logit, meta, row_of, loss, lse);
+    return e != cudaSuccess ? e : cudaPeekAtLastError();
+}
+
+cudaError_t launch_vocab_dx_join(const float *part, int splits, long long split_stride, const VocabMeta *meta,
+                                 const int *packed_of, int T, int H, uint16_t *d_hidden, cudaStream_t s)
+{
+    const int blocks = T < 2432 ? T : 2432;
+    const cudaError_t e = launch_pdl(vocab_dx_join_kernel, dim3(blocks), dim3(128), 0, s, part, splits, split_stride,
+                                     meta, packed_of, T, H, d_hidden);
+    return e != cudaSuccess ? e : cudaPeekAtLastError();
+}
+
+}  // namespace glr

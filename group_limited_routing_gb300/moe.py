@@ -470,6 +470,181 @@ def rmsnorm(x, eps: float = 1e-6, out=None):
     return out
 
 
+def block_norm_workspace(T: int, H: int, groups: int = 1, device=None) -> SizedWorkspace:
+    """The workspace of block_norm_backward."""
+    return SizedWorkspace(_lib.load().moe_block_norm_workspace_bytes(T, H, groups), "moe_block_norm_backward", device)
+
+
+def _block_norm_args(x, y, gate, w_post, w_pre):
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise TypeError("x must be a [T, H] tensor")
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("x must be torch.bfloat16 or torch.float32, got %s" % x.dtype)
+    dev = x.device
+    T, H = x.shape
+    groups = 1 if gate is None else gate.shape[0]
+    px = _need(x, "x", x.dtype, (T, H), dev)
+    py = _opt(y, "y", torch.bfloat16, (T, H), dev)
+    pg = _opt(gate, "gate", torch.float32, (groups, H), dev)
+    pp = _opt(w_post, "w_post", torch.float32, (H,), dev)
+    pq = _opt(w_pre, "w_pre", torch.float32, (H,), dev)
+    return T, H, groups, int(x.dtype == torch.float32), px, py, pg, pp, pq
+
+
+def block_norm(x, y=None, gate=None, w_post=None, w_pre=None, *, alpha: float = 1.0, eps: float = 1e-6, out=None):
+    """moe_block_norm: (r, n) with r = alpha x + gate RMS(y) w_post (the new
+    residual stream, x's type) and n = RMS(r) w_pre (the next block's input,
+    bf16).  x [T, H] bf16 or fp32, y [T, H] bf16 (None: r = alpha x), gate
+    [groups, H] fp32 with T % groups == 0, w_post and w_pre [H] fp32 (None: 1).
+    `out` = (r, n) is filled instead of allocating; r may be x, n may be y."""
+    T, H, groups, f32, px, py, pg, pp, pq = _block_norm_args(x, y, gate, w_post, w_pre)
+    dev = x.device
+    r, n = out if out is not None else (torch.empty_like(x), torch.empty(T, H, dtype=torch.bfloat16, device=dev))
+    pr = _need(r, "r", x.dtype, (T, H), dev)
+    pn = _need(n, "n", torch.bfloat16, (T, H), dev)
+    _lib.check(_lib.load().moe_block_norm(T, H, groups, f32, px, py, pg, pp, pq, alpha, eps, pr, pn, _stream(dev)),
+               "moe_block_norm")
+    return r, n
+
+
+def block_norm_backward(x, y, gate, w_post, w_pre, d_r, d_n, *, alpha: float = 1.0, eps: float = 1e-6,
+                        ws: Optional[SizedWorkspace] = None, out: Optional[dict] = None):
+    """moe_block_norm_backward: the gradients of block_norm(x, y, gate, w_post,
+    w_pre) from d_r [T, H] (x's type; None: zero) and d_n [T, H] bf16, as
+    dict(d_x, d_y, d_gate [groups, H], dw_post [H], dw_pre [H]), the vectors in
+    fp32; without y only d_x and dw_pre.  `out` (a dict like the result) is
+    filled instead of allocating; its d_x may be d_r, its d_y may be d_n."""
+    T, H, groups, f32, px, py, pg, pp, pq = _block_norm_args(x, y, gate, w_post, w_pre)
+    dev = x.device
+    pdr = _opt(d_r, "d_r", x.dtype, (T, H), dev)
+    pdn = _need(d_n, "d_n", torch.bfloat16, (T, H), dev)
+    vec = torch.float32
+    shapes = dict(d_x=((T, H), x.dtype), dw_pre=((H,), vec))
+    if y is not None:
+        shapes.update(d_y=((T, H), torch.bfloat16), d_gate=((groups, H), vec), dw_post=((H,), vec))
+    g = {}
+    for name, (shape, dt) in shapes.items():
+        t = out.get(name) if out else None
+        if t is None:
+            t = torch.empty(*shape, dtype=dt, device=dev)
+        _need(t, name, dt, shape, dev)
+        g[name] = t
+    need = int(_lib.load().moe_block_norm_workspace_bytes(T, H, groups))
+    if need and (ws is None or ws.nbytes < need):
+        ws = SizedWorkspace(need, "moe_block_norm_backward", dev)
+    # (an unsupported shape has no workspace size: the call itself names the error)
+    ptr = {name: t.data_ptr() for name, t in g.items()}
+    rc = _lib.load().moe_block_norm_backward(T, H, groups, f32, px, py, pg, pp, pq, alpha, eps, pdr, pdn, ptr["d_x"],
+                                             ptr.get("d_y"), ptr.get("d_gate"), ptr.get("dw_post"), ptr["dw_pre"],
+                                             ws.ptr if need else None, ws.nbytes if need else 0, _stream(dev))
+    _lib.check(rc, "moe_block_norm_backward")
+    return g
+
+
+def vocab_loss_workspace(T: int, H: int, V: int, backward: bool = False, device=None) -> SizedWorkspace:
+    """The workspace of vocab_loss, or with backward=True of vocab_loss_backward."""
+    return SizedWorkspace(_lib.load().moe_vocab_loss_workspace_bytes(T, H, V, int(backward)), "moe_vocab_loss",
+                          device)
+
+
+def _vocab_args(hidden, W_vocab, target, backward, ws):
+    for name, t in (("hidden", hidden), ("W_vocab", W_vocab)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            raise TypeError("%s must be a 2-dimensional tensor" % name)
+    dev = hidden.device
+    T, H = hidden.shape
+    V = W_vocab.shape[0]
+    ph = _need(hidden, "hidden", torch.bfloat16, (T, H), dev)
+    pw = _need(W_vocab, "W_vocab", torch.bfloat16, (V, H), dev)
+    if not isinstance(target, torch.Tensor) or target.dtype not in (torch.int32, torch.int64):
+        raise TypeError("target must be a torch.int32 or torch.int64 tensor")
+    pt = _need(target, "target", target.dtype, (T,), dev)
+    need = int(_lib.load().moe_vocab_loss_workspace_bytes(T, H, V, int(backward)))
+    if need and (ws is None or ws.nbytes < need):
+        ws = SizedWorkspace(need, "moe_vocab_loss", dev)
+    # (an unsupported shape has no workspace size: the call itself names the error;
+    # the caller holds on to ws until the launches are enqueued)
+    bits = 64 if target.dtype == torch.int64 else 32
+    return (T, H, V, ph, pw, pt, bits), (ws.ptr if need else None, ws.nbytes if need else 0, _stream(dev)), ws
+
+
+def vocab_loss(hidden, W_vocab, target, *, ignore_index: int = -100, ws: Optional[SizedWorkspace] = None, out=None):
+    """moe_vocab_loss: (loss [T] fp32, lse [T] fp32) of the softmax cross entropy
+    of hidden [T, H] bf16 over the vocabulary W_vocab [V, H] bf16; target [T]
+    int32 or int64, rows with target == ignore_index give zeros.  No reduction:
+    the mean is loss.sum() / (rows that count).  `out` = (loss, lse) is filled
+    instead of allocating."""
+    a, z, ws = _vocab_args(hidden, W_vocab, target, False, ws)
+    T, dev = a[0], hidden.device
+    loss, lse = out if out is not None else (torch.empty(T, dtype=torch.float32, device=dev) for _ in range(2))
+    pl = _need(loss, "loss", torch.float32, (T,), dev)
+    pe = _need(lse, "lse", torch.float32, (T,), dev)
+    _lib.check(_lib.load().moe_vocab_loss(*a, ignore_index, pl, pe, *z), "moe_vocab_loss")
+    return loss, lse
+
+
+def vocab_loss_backward(hidden, W_vocab, target, lse, d_loss, *, ignore_index: int = -100,
+                        ws: Optional[SizedWorkspace] = None, out: Optional[dict] = None):
+    """moe_vocab_loss_backward: dict(d_hidden [T, H] bf16, dW_vocab [V, H] bf16)
+    from d_loss [T] fp32 (1 / n on every row for the mean over n) and vocab_loss's
+    lse; `out` (a dict like the result) is filled instead of allocating."""
+    a, z, ws = _vocab_args(hidden, W_vocab, target, True, ws)
+    T, dev = a[0], hidden.device
+    pe = _need(lse, "lse", torch.float32, (T,), dev)
+    pd = _need(d_loss, "d_loss", torch.float32, (T,), dev)
+    g = {}
+    for name, like in (("d_hidden", hidden), ("dW_vocab", W_vocab)):
+        t = out.get(name) if out else None
+        if t is None:
+            t = torch.empty_like(like)
+        _need(t, name, torch.bfloat16, like.shape, dev)
+        g[name] = t
+    _lib.check(_lib.load().moe_vocab_loss_backward(*a, ignore_index, pe, pd, g["d_hidden"].data_ptr(),
+                                                   g["dW_vocab"].data_ptr(), *z), "moe_vocab_loss_backward")
+    return g
+
+
+def route_backward_workspace(cfg: MoeConfig, device=None) -> SizedWorkspace:
+    """The workspace of route_backward."""
+    return SizedWorkspace(_lib.load().moe_route_backward_workspace_bytes(ctypes.byref(cfg.c())),
+                          "moe_route_backward", device)
+
+
+def route_backward(cfg: MoeConfig, hidden, W_router, topk_idx, d_topk_w, *, d_aux_loss=None, expert_counts=None,
+                   d_hidden_add=None, W_split=None, ws: Optional[SizedWorkspace] = None, out: Optional[dict] = None):
+    """moe_route_backward: the router's gradient for route()'s choice of experts,
+    dict(d_hidden [T, H] bf16, dW_router [E, H] fp32), from d_topk_w [T, k]
+    (backward()'s) and optionally d_aux_loss [1] with route()'s expert_counts;
+    d_hidden_add [T, H] (backward()'s d_hidden) is added before the rounding.
+    `out` (a dict like the result) is filled instead of allocating; its d_hidden
+    may be d_hidden_add."""
+    dev = hidden.device
+    bf, f32 = torch.bfloat16, torch.float32
+    ph = _need(hidden, "hidden", bf, (cfg.T, cfg.H), dev)
+    pw = _need(W_router, "W_router", f32, (cfg.E, cfg.H), dev)
+    ps = _opt(W_split, "W_split", bf, (3, cfg.E, cfg.H), dev)
+    pi = _need(topk_idx, "topk_idx", torch.int32, (cfg.T, cfg.k), dev)
+    pd = _need(d_topk_w, "d_topk_w", f32, (cfg.T, cfg.k), dev)
+    pc = _opt(expert_counts, "expert_counts", torch.int32, (cfg.E,), dev)
+    pa = _opt(d_aux_loss, "d_aux_loss", f32, (1,), dev)
+    pp = _opt(d_hidden_add, "d_hidden_add", bf, (cfg.T, cfg.H), dev)
+    g = {}
+    for name, shape, dt in (("d_hidden", (cfg.T, cfg.H), bf), ("dW_router", (cfg.E, cfg.H), f32)):
+        t = out.get(name) if out else None
+        if t is None:
+            t = torch.empty(*shape, dtype=dt, device=dev)
+        _need(t, name, dt, shape, dev)
+        g[name] = t
+    need = int(_lib.load().moe_route_backward_workspace_bytes(ctypes.byref(cfg.c())))
+    if need and (ws is None or ws.nbytes < need):
+        ws = SizedWorkspace(need, "moe_route_backward", dev)
+    rc = _lib.load().moe_route_backward(ctypes.byref(cfg.c()), ph, pw, ps, pi, pd, pc, pa, pp,
+                                        g["d_hidden"].data_ptr(), g["dW_router"].data_ptr(),
+                                        ws.ptr if need else None, ws.nbytes if need else 0, _stream(dev))
+    _lib.check(rc, "moe_route_backward")
+    return g
+
+
 def last_launch_count() -> int:
     """Kernels the last call on this thread enqueued."""
     return int(_lib.load().moe_last_launch_count())

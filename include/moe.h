@@ -81,6 +81,7 @@ typedef struct moe_cfg {
 #define MOE_STATUS_BAD_EXPERT_INDEX 2  /* topk_idx held an id outside [0, E)     */
 #define MOE_STATUS_TIMEOUT 4           /* a bounded device wait ran out          */
 #define MOE_STATUS_COUNT_MISMATCH 8    /* bucketed rows != k*T (follows from 2)  */
+#define MOE_STATUS_BAD_TARGET 16       /* a target outside [0, V), not the ignored one */
 
 /* workspace kinds */
 #define MOE_WS_ROUTE 0
@@ -387,6 +388,97 @@ int moe_expert_feedback(const moe_cfg *cfg, const int32_t *expert_counts, float 
  * x, out [T, H] bf16 (may alias), H % 8 == 0, 16-byte aligned. */
 int moe_rmsnorm(int32_t T, int32_t H, const moe_bf16 *x, moe_bf16 *out, float eps, void *stream);
 
+/* ---- Training operators ----------------------------------------------------
+ * What a training step of a stack of these layers needs beside moe_backward:
+ * the norms around a block, the loss over the vocabulary and the router's
+ * gradient.  The pages train the model but print none of these; the formulas
+ * below define them.
+ *
+ * Norms around a block, fused with the block's gate and the residual scale.
+ * With RMS(z) = z / sqrt(mean_h z^2 + eps), x the residual stream, y the
+ * block's output:
+ *   r = alpha x + gate RMS(y) w_post      (y NULL: r = alpha x)
+ *   n = RMS(r) w_pre                      (from r before r is rounded)
+ *   x      [T, H], bf16 (stream_f32 = 0) or fp32 (1)
+ *   y      [T, H] bf16, or NULL: the norm in front of a stack's first block
+ *   gate   [groups, H] fp32, or NULL for 1; row t takes gate row
+ *          t / (T / groups): one for all tokens, for each sequence or each token
+ *   w_post, w_pre [H] fp32, or NULL for 1
+ *   r      [T, H] out, x's type (may alias x; may be NULL when y is)
+ *   n      [T, H] bf16 out (may alias y)
+ * fp32 arithmetic, each output rounded once.  H % 8 == 0, H <= 8192,
+ * T % groups == 0, pointers 16-byte aligned.  gate and w_post need y. */
+int moe_block_norm(int32_t T, int32_t H, int32_t groups, int32_t stream_f32, const void *x, const moe_bf16 *y,
+                   const float *gate, const float *w_post, const float *w_pre, float alpha, float eps, void *r,
+                   moe_bf16 *n, void *stream);
+
+/* Gradient of moe_block_norm, from d_r [T, H] (x's type; NULL for zero) and
+ * d_n [T, H] bf16:
+ *   d_x    [T, H] out, x's type (may alias d_r), d_y [T, H] bf16 out (may alias
+ *          d_n; NULL without y)
+ *   d_gate [groups, H], dw_post [H], dw_pre [H] fp32 out, overwritten; each may
+ *          be NULL (with gate, w_post or w_pre NULL they are the gradients at 1)
+ * x and y are the forward's inputs; nothing else is kept from it.  Workspace of
+ * moe_block_norm_workspace_bytes(T, H, groups) bytes.  Deterministic. */
+size_t moe_block_norm_workspace_bytes(int32_t T, int32_t H, int32_t groups);
+int moe_block_norm_backward(int32_t T, int32_t H, int32_t groups, int32_t stream_f32, const void *x,
+                            const moe_bf16 *y, const float *gate, const float *w_post, const float *w_pre,
+                            float alpha, float eps, const void *d_r, const moe_bf16 *d_n, void *d_x, moe_bf16 *d_y,
+                            float *d_gate, float *dw_post, float *dw_pre, void *ws, size_t ws_bytes, void *stream);
+
+/* Softmax cross entropy of T hidden states over a vocabulary of V, formed from
+ * the head's weight in pieces, without the [T, V] logits in memory:
+ *   z[t, v] = <hidden[t], W_vocab[v]>, lse[t] = log sum_v exp z[t, v],
+ *   loss[t] = lse[t] - z[t, target[t]]
+ * and loss = lse = 0 where target[t] == ignore_index.  A target outside [0, V)
+ * that is not ignore_index counts as ignored and sets MOE_STATUS_BAD_TARGET.
+ * Rows that do not count are neither read nor multiplied.
+ *   hidden   [T, H] bf16, H % 8 == 0, H <= 65536 (T == 0: nothing is done)
+ *   W_vocab  [V, H] bf16, any V
+ *   target   [T] int32 or int64 (target_bits 32 or 64)
+ *   loss, lse [T] fp32 out
+ * Products of bf16 in fp32 on the tensor cores; the softmax in fp32.
+ * Workspace of moe_vocab_loss_workspace_bytes(T, H, V, 0) bytes.
+ * Deterministic. */
+size_t moe_vocab_loss_workspace_bytes(int32_t T, int32_t H, int32_t V, int backward);
+int moe_vocab_loss(int32_t T, int32_t H, int32_t V, const moe_bf16 *hidden, const moe_bf16 *W_vocab,
+                   const void *target, int32_t target_bits, int64_t ignore_index, float *loss, float *lse, void *ws,
+                   size_t ws_bytes, void *stream);
+
+/* Gradient of moe_vocab_loss from d_loss [T] fp32 (dL/d loss[t]; not read where
+ * the row does not count) and the forward's lse [T]:
+ *   dz[t, v] = d_loss[t] (exp(z[t, v] - lse[t]) - [v == target[t]])
+ *   d_hidden [T, H] bf16 out = dz W_vocab, zero rows where the row does not count
+ *   dW_vocab [V, H] bf16 out = dz^T hidden, overwritten
+ * The logits are formed again, a piece of the vocabulary at a time; dz is
+ * rounded to bf16 as an operand of the two products (relative to the largest
+ * |d_loss|), whose sums are fp32 and rounded once.  Workspace of
+ * moe_vocab_loss_workspace_bytes(T, H, V, 1) bytes: dz of one piece (1 GiB at
+ * most, or 256 columns of it) and fp32 sums of d_hidden.  Deterministic. */
+int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hidden, const moe_bf16 *W_vocab,
+                            const void *target, int32_t target_bits, int64_t ignore_index, const float *lse,
+                            const float *d_loss, moe_bf16 *d_hidden, moe_bf16 *dW_vocab, void *ws, size_t ws_bytes,
+                            void *stream);
+
+/* The router's gradient for a fixed choice of experts: what moe_backward leaves
+ * out.  From d_topk_w [T, k] fp32 (moe_backward's) and, when d_aux_loss [1] fp32
+ * is given, that of the balance loss (expert_counts [E] as moe_route wrote them,
+ * held fixed), through the normalised weights and the sigmoid scores:
+ *   d_hidden  [T, H] bf16 out = dL W_router (+ d_hidden_add [T, H] bf16, e.g.
+ *             moe_backward's d_hidden; NULL for none; may be d_hidden itself)
+ *   dW_router [E, H] fp32 out = dL^T hidden, overwritten
+ * with dL [T, E] the gradient of the logits, which are formed again (fp32, as
+ * in moe_route).  W_split as in moe_layer (NULL: split here).  The selection
+ * itself, and so expert_bias, has no gradient.  An expert id outside [0, E) is
+ * skipped (MOE_STATUS_BAD_EXPERT_INDEX); non-finite logits set
+ * MOE_STATUS_NONFINITE_LOGIT.  Same shapes as moe_route; workspace of
+ * moe_route_backward_workspace_bytes(cfg) bytes.  Deterministic. */
+size_t moe_route_backward_workspace_bytes(const moe_cfg *cfg);
+int moe_route_backward(const moe_cfg *cfg, const moe_bf16 *hidden, const float *W_router, const moe_bf16 *W_split,
+                       const int32_t *topk_idx, const float *d_topk_w, const int32_t *expert_counts,
+                       const float *d_aux_loss, const moe_bf16 *d_hidden_add, moe_bf16 *d_hidden, float *dW_router,
+                       void *ws, size_t ws_bytes, void *stream);
+
 /* Waits for `stream`, then copies the workspace's status word (MOE_STATUS_*
  * bits, OR-ed over every call since the last reset) to *status (a HOST
  * pointer); clears it when reset != 0.  Returns MOE_OK, or MOE_ERR_CUDA. */
@@ -409,8 +501,8 @@ int moe_last_launch_count(void);
  * events, folds them into per-kernel totals and returns the total
  * milliseconds and interval count of `kernel_id` (0 <= kernel_id <
  * MOE_KERNEL_COUNT), clearing them when reset != 0. */
-#define MOE_KERNEL_COUNT 19
-#define MOE_KERNEL_STAGE_ROUTE_PERMUTE 18
+#define MOE_KERNEL_COUNT 30
+#define MOE_KERNEL_STAGE_ROUTE_PERMUTE 29
 int moe_profile_enable(int on);
 int moe_profile_read(int kernel_id, double *total_ms, int32_t *launches, int reset);
 const char *moe_kernel_name(int kernel_id);
