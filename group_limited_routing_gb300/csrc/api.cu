@@ -838,15 +838,12 @@ namespace host {
 
 size_t route_region_bytes(const moe_cfg &c) { return route_layout(c).total; }
 
-uint16_t *route_region_split(const moe_cfg &c, void *ws) { return at<uint16_t>(ws, route_layout(c).w3); }
-
 int route_region_logits(const moe_cfg &c, const moe_bf16 *hidden, const float *W, const moe_bf16 *W_split, void *ws,
-                        int sms, cudaStream_t s, int &launches, float **logits)
+                        int sms, cudaStream_t s, int &launches, float **logits, int *nparts)
 {
     const RouteLayout L = route_layout(c);
-    int nparts = 1;
     *logits = at<float>(ws, L.logits);
-    return router_gemm(c, hidden, W, W_split, *logits, nullptr, ws, L, sms, s, launches, 1, nparts);
+    return router_gemm(c, hidden, W, W_split, *logits, nullptr, ws, L, sms, s, launches, L.ksplit, *nparts);
 }
 
 }  // namespace host

@@ -53,17 +53,21 @@ int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 // K splits of a product with few output tiles: the number that finishes
 // soonest when a pair takes units of kblocks / splits K blocks one after the
-// other, each with an epilogue that costs about EPILOGUE_BLOCKS more.  It
+// other, each with an epilogue that costs about EPILOGUE_BLOCKS more, and every
+// split's sums (`elements` of them) are written and read once more.  One K block
+// takes a pair 0.27 us, in which HBM moves 450,000 fp32 values.  The number
 // depends on the shape alone, so results do not change with the device's load.
-constexpr int EPILOGUE_BLOCKS = 6, MAX_SPLITS = 16, MIN_BLOCKS = 8;
+constexpr int EPILOGUE_BLOCKS = 4;
+constexpr double ELEMENTS_PER_BLOCK = 450e3;
 
-int choose_splits(int tiles, int kblocks, int max_splits = MAX_SPLITS)
+int choose_splits(int tiles, int kblocks, double elements, int max_splits, int min_blocks)
 {
     int best = 1;
     double best_cost = 0.0;
-    for (int n = 1; n <= max_splits && (n == 1 || kblocks / n >= MIN_BLOCKS); ++n) {
-        const double cost = (double)ceil_div((long long)tiles * n, PAIRS) * ((double)kblocks / n + EPILOGUE_BLOCKS) +
-                            0.5 * n;
+    for (int n = 1; n <= max_splits && (n == 1 || kblocks / n >= min_blocks); ++n) {
+        const double cost = (double)ceil_div((long long)tiles * n, PAIRS) *
+                                (ceil_div(kblocks, n) + EPILOGUE_BLOCKS) +
+                            2.0 * n * elements / ELEMENTS_PER_BLOCK;
         if (n == 1 || cost < best_cost) {
             best = n;
             best_cost = cost;
@@ -71,6 +75,11 @@ int choose_splits(int tiles, int kblocks, int max_splits = MAX_SPLITS)
     }
     return best;
 }
+
+// K blocks per accumulator of the loss's logits (512 of K): the tensor core's
+// own running sum then stays as close to the exact one as an fp32 library
+// product's (measured, 2-norm over a batch's losses at H = 2048: PLACEHOLDER)
+constexpr int LOGIT_PART_BLOCKS = 8;
 
 // ---------------------------------------------------------- vocabulary loss
 int check_vocab(int32_t T, int32_t H, int32_t V, int32_t target_bits)
@@ -89,7 +98,7 @@ constexpr size_t VOCAB_PIECE_BYTES = 1ull << 30;
 
 struct VocabLayout {
     size_t meta, row_of, target, packed_of, lse, weight, logit, stats, hidden, dz, part, total;
-    int ntiles, piece, splits, split_rows;
+    int ntiles, nstats, piece, splits, split_rows;
 };
 
 VocabLayout vocab_layout(int T, int H, int V, bool backward)
@@ -103,6 +112,7 @@ VocabLayout vocab_layout(int T, int H, int V, bool backward)
         return at;
     };
     L.ntiles = ceil_div(V, 256);
+    L.nstats = ceil_div(V, 128);
     L.meta = take(sizeof(VocabMeta));
     L.row_of = take(4ull * T);
     L.target = take(4ull * T);
@@ -115,11 +125,11 @@ VocabLayout vocab_layout(int T, int H, int V, bool backward)
         L.piece = (int)std::min<size_t>(L.ntiles, most) * 256;
         L.dz = take(2ull * T * L.piece);
         L.split_rows = ceil_div(T, 256) * 256;
-        L.splits = choose_splits(ceil_div(T, 256) * ceil_div(H, 256), L.piece / GEMM_BK);
+        L.splits = choose_splits(ceil_div(T, 256) * ceil_div(H, 256), L.piece / GEMM_BK, (double)T * H, 16, 8);
         L.part = take(4ull * L.splits * L.split_rows * H);
     } else {
         L.logit = take(4ull * T);
-        L.stats = take(sizeof(float2) * (size_t)L.ntiles * T);
+        L.stats = take(sizeof(float2) * (size_t)L.nstats * T);
     }
     L.total = off;
     return L;
@@ -144,9 +154,8 @@ struct RouteBwdLayout {
     int splits;
 };
 
-// K of the weight gradient is the tokens: at most this many 64-token blocks
-// per split, so that the tensor core's own fp32 accumulation stays short.
-constexpr int ROUTE_DW_BLOCKS = 16;
+// 64-token blocks per accumulator of the weight gradient (its K is the tokens)
+constexpr int ROUTE_DW_BLOCKS = 8;
 
 RouteBwdLayout route_bwd_layout(const moe_cfg &c)
 {
@@ -159,9 +168,7 @@ RouteBwdLayout route_bwd_layout(const moe_cfg &c)
     };
     L.split = take(3ull * c.E * c.H * 2);
     L.parts = take(3ull * c.T * c.E * 2);
-    const int kblocks = ceil_div(c.T, GEMM_BK);
-    L.splits = std::max(1, std::max(ceil_div(kblocks, ROUTE_DW_BLOCKS),
-                                    std::min(kblocks, PAIRS / ceil_div(c.H, 256))));
+    L.splits = choose_splits(ceil_div(c.H, 256), 3 * ceil_div(c.T, GEMM_BK), 256.0 * c.H, 64, 3);
     L.part = take(4ull * L.splits * 256 * c.H);
     L.total = off;
     return L;
@@ -321,6 +328,7 @@ int moe_vocab_loss(int32_t T, int32_t H, int32_t V, const moe_bf16 *hidden, cons
     p.N = V;
     p.nseg = 1;
     p.kblocks = ceil_div(H, GEMM_BK);
+    p.part_blocks = LOGIT_PART_BLOCKS;
     p.splits = 1;
     p.group_m = vocab_group(H);
     p.target = rp.packed_target;
@@ -329,7 +337,7 @@ int moe_vocab_loss(int32_t T, int32_t H, int32_t V, const moe_bf16 *hidden, cons
     p.target_logit = at<float>(ws, L.logit);
     p.status = status;
     GLR_LAUNCH(KID_VOCAB_LOGITS, launch_pair_gemm(PG_STATS, false, false, p, ceil_div(T, 256) * L.ntiles, s));
-    GLR_LAUNCH(KID_VOCAB_JOIN, launch_vocab_join(p.stats, L.ntiles, T, p.target_logit, meta, rp.row_of, T, loss, lse,
+    GLR_LAUNCH(KID_VOCAB_JOIN, launch_vocab_join(p.stats, L.nstats, T, p.target_logit, meta, rp.row_of, T, loss, lse,
                                                  s));
     set_last_launches(launches);
     return MOE_OK;
@@ -394,7 +402,7 @@ int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hid
     pz.meta = meta;
     pz.m_from_rows = 1;
     pz.nseg = 1;
-    pz.kblocks = ceil_div(H, GEMM_BK);
+    pz.kblocks = pz.part_blocks = ceil_div(H, GEMM_BK);
     pz.splits = 1;
     pz.group_m = vocab_group(H);
     pz.out_rows = T;
@@ -427,6 +435,7 @@ int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hid
     pw.T = T;
     pw.meta = meta;
     pw.k_from_rows = 1;
+    pw.part_blocks = ceil_div(T, GEMM_BK);
     pw.N = H;
     pw.nseg = 1;
     pw.splits = 1;
@@ -441,7 +450,7 @@ int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hid
         pz.b_off[0] = v0;
         GLR_LAUNCH(KID_VOCAB_DLOGITS,
                    launch_pair_gemm(PG_DLOGITS, false, false, pz, m_tiles * ceil_div(n, 256), s));
-        px.kblocks = ceil_div(n, GEMM_BK);
+        px.kblocks = px.part_blocks = ceil_div(n, GEMM_BK);
         px.b_off[0] = v0;
         px.accumulate = v0 > 0;
         GLR_LAUNCH(KID_VOCAB_DX, launch_pair_gemm(PG_PARTIAL, false, true, px, m_tiles * h_tiles * L.splits, s));
@@ -492,10 +501,11 @@ int moe_route_backward(const moe_cfg *cfg, const moe_bf16 *hidden, const float *
         W3 = own;
     }
     float *logits = nullptr;
-    if ((rc = route_region_logits(c, hidden, W_router, W3, ws, sms, s, launches, &logits)) != MOE_OK)
+    int nparts = 1;
+    if ((rc = route_region_logits(c, hidden, W_router, W3, ws, sms, s, launches, &logits, &nparts)) != MOE_OK)
         return rc;
     uint16_t *parts = at<uint16_t>(ws, L.parts);
-    GLR_LAUNCH(KID_ROUTE_BWD_SCORES, launch_route_grad(logits, topk_idx, d_topk_w, expert_counts, d_aux_loss, c.T, c.E,
+    GLR_LAUNCH(KID_ROUTE_BWD_SCORES, launch_route_grad(logits, nparts, topk_idx, d_topk_w, expert_counts, d_aux_loss, c.T, c.E,
                                                        c.k, c.rsf, c.eps, parts, status, s));
     const int h_tiles = ceil_div(c.H, 256);
     // d_hidden = dL W: of the parts' products the three largest (the rest is
@@ -508,16 +518,17 @@ int moe_route_backward(const moe_cfg *cfg, const moe_bf16 *hidden, const float *
     p.M = c.T;
     p.N = c.H;
     p.nseg = 3;
-    p.kblocks = c.E / GEMM_BK;
+    p.kblocks = p.part_blocks = c.E / GEMM_BK;
     p.a_off[0] = c.T;              // middle x high
     p.b_off[1] = c.E;              // high x middle
     p.splits = 1;                  // (third segment: high x high)
     p.group_m = 1;
     p.out_rows = c.T;
     p.out_cols = c.H;
-    p.add = d_hidden_add;
     p.status = status;
-    GLR_LAUNCH(KID_ROUTE_BWD_DX, launch_pair_gemm(PG_BF16, false, true, p, ceil_div(c.T, 256) * h_tiles, s));
+    if (d_hidden_add && !make_map_bf16(&p.tmHidden, d_hidden_add, c.T, c.H, 64, 32))
+        return MOE_ERR_CUDA;
+    GLR_LAUNCH(KID_ROUTE_BWD_DX, launch_pair_gemm(d_hidden_add ? PG_BF16_ADD : PG_BF16, false, true, p, ceil_div(c.T, 256) * h_tiles, s));
     // dW = dL^T hidden, exact products: low, middle, high part of dL
     float *part = at<float>(ws, L.part);
     memset(&p, 0, sizeof(p));
@@ -529,6 +540,7 @@ int moe_route_backward(const moe_cfg *cfg, const moe_bf16 *hidden, const float *
     p.N = c.H;
     p.nseg = 3;
     p.kblocks = ceil_div(c.T, GEMM_BK);
+    p.part_blocks = ROUTE_DW_BLOCKS;
     p.a_off[0] = 2 * c.T;
     p.a_off[1] = c.T;
     p.splits = L.splits;

@@ -67,13 +67,11 @@ bool make_map_f32(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols,
                   uint32_t box_rows);
 
 // The routing region at the start of a workspace (header first) and the fp32
-// logits [T, E] computed into it (one buffer, no K parts) with the weight's
-// bf16 x 3 split W_split.
+// logits [T, E] computed into it with the weight's bf16 x 3 split W_split, as
+// *nparts buffers T E floats apart whose sum they are (the router GEMM's K parts).
 size_t route_region_bytes(const moe_cfg &c);
 int route_region_logits(const moe_cfg &c, const moe_bf16 *hidden, const float *W, const moe_bf16 *W_split, void *ws,
-                        int sms, cudaStream_t s, int &launches, float **logits);
-// where the region keeps a split of its own [3, E, H]
-uint16_t *route_region_split(const moe_cfg &c, void *ws);
+                        int sms, cudaStream_t s, int &launches, float **logits, int *nparts);
 
 }  // namespace host
 }  // namespace glr

@@ -336,8 +336,9 @@ cudaError_t launch_expert_feedback(const int32_t *counts, int E, int T, int k, f
 //   PG_STATS    the columns' softmax statistics per row, and the target's logit
 //   PG_DLOGITS  bf16( weight (exp(z - lse) - [n = target]) )
 //   PG_PARTIAL  fp32, stored or added to what is there (one slice per K split)
-//   PG_BF16     bf16( scale z (+ add) )
-enum PairEpilogue { PG_STATS = 0, PG_DLOGITS = 1, PG_PARTIAL = 2, PG_BF16 = 3 };
+//   PG_BF16     bf16( scale z )
+//   PG_BF16_ADD bf16( z + add )
+enum PairEpilogue { PG_STATS = 0, PG_DLOGITS = 1, PG_PARTIAL = 2, PG_BF16 = 3, PG_BF16_ADD = 4 };
 
 // What the vocabulary operators' row kernel leaves for the kernels after it.
 struct VocabMeta {
@@ -347,7 +348,9 @@ struct VocabMeta {
 
 struct PairGemmParams {
     CUtensorMap tmA, tmB, tmOut;
-    CUtensorMap tmHidden;     // the rows that count, packed: replaces A (STATS, DLOGITS) or B (BF16) when they are fewer than T
+    // the rows that count, packed: replaces A (STATS, DLOGITS) or B (BF16) when
+    // they are fewer than T; BF16_ADD: the addend, boxes of 64 columns x 32 rows
+    CUtensorMap tmHidden;
     int T;                    // rows of `hidden`
     const VocabMeta *meta;    // NULL: M and kblocks as given
     int m_from_rows;          // M = meta->rows
@@ -355,7 +358,8 @@ struct PairGemmParams {
     int M, N;
     int nseg, kblocks;        // K = nseg segments of kblocks blocks of 64
     int a_off[3], b_off[3];   // per segment: rows added to the operand's row coordinate
-    int splits;               // K range cut into this many parts (inside every segment)
+    int splits;               // K range cut among this many units (inside every segment)
+    int part_blocks;          // blocks per segment and accumulator (STATS, PARTIAL; else at least kblocks)
     int group_m;              // tiles run m-fastest within groups of this many m-tiles
     int out_row0;             // row of the output map where row 0 goes
     int out_rows, out_cols;   // the output map's extent
@@ -364,12 +368,10 @@ struct PairGemmParams {
     // PG_STATS, PG_DLOGITS
     const int *target;        // per packed row
     int n0;                   // vocabulary id of column 0
-    float2 *stats;            // [n-tiles][ld_stats] (base of the exponentials in log2, their sum)
+    float2 *stats;            // [128-column blocks][ld_stats] (base of the exponentials in log2, their sum)
     int ld_stats;
     float *target_logit;      // per packed row
     const float *lse, *weight; // per packed row
-    // PG_BF16
-    const uint16_t *add;      // [out_rows, N] or NULL
     int *status;
 };
 cudaError_t launch_pair_gemm(PairEpilogue epi, bool a_mn, bool b_mn, const PairGemmParams &p, int max_units,
@@ -400,7 +402,8 @@ cudaError_t launch_vocab_dx_join(const float *part, int splits, long long split_
                                  const int *packed_of, int T, int H, uint16_t *d_hidden, cudaStream_t s);
 
 // ---- the router's gradient (route_grad.cu) --------------------------------------
-cudaError_t launch_route_grad(const float *logits, const int32_t *idx, const float *d_w, const int32_t *counts,
+// (logits: nparts buffers of [T, E], one after the other, to be added)
+cudaError_t launch_route_grad(const float *logits, int nparts, const int32_t *idx, const float *d_w, const int32_t *counts,
                               const float *d_aux, int T, int E, int k, float rsf, float eps, uint16_t *parts,
                               int *status, cudaStream_t s);
 // out[i] = sum over the splits of part[s stride + i], i < n

@@ -13,9 +13,16 @@
 // softmax work of the loss (PG_STATS, PG_DLOGITS) is in the epilogue, so the
 // [rows, vocabulary] logits exist in TMEM only.
 //
-// Roles (192 threads): warp 0 lane 0 loads, warp 1 lane 0 of the even CTA
+// The tensor core does not round its running fp32 sum to nearest: over a long K
+// the sum drifts by several times an fp32 product's error.  Where the result
+// stays fp32 (the loss, the router weight's gradient), K is cut into parts:
+// each part has an accumulator of its own, and the epilogue warps add the
+// parts in registers, rounding to nearest.
+//
+// Roles (320 threads): warp 0 lane 0 loads, warp 1 lane 0 of the even CTA
 // issues the MMAs (of the odd one, forwards its epilogue's arrivals to the
-// even one), warps 2..5 run the epilogue on the TMEM lanes 32 (w % 4) .. + 31.
+// even one), warps 2..9 run the epilogue: TMEM lanes 32 (w % 4) .. + 31, the
+// tile's left or right 128 columns.
 // Every wait is bounded; when one runs out, every role leaves its loop, copies
 // in flight are waited for (bounded), TMEM is freed and the status word gets
 // MOE_STATUS_TIMEOUT.
@@ -30,20 +37,28 @@ namespace glr {
 
 namespace {
 
-constexpr int PG_THREADS = 64 + 32 * 4;
+constexpr int PG_EPI_WARPS = 8;
+constexpr int PG_THREADS = 64 + 32 * PG_EPI_WARPS;
 constexpr int PG_BM = 256, PG_BN = 256;          // a pair's tile
+constexpr int PG_HALF = PG_BN / 2;               // an epilogue warp's columns
 constexpr float LOG2E = 1.44269504088896341f;
 
+constexpr int PG_ATOM = 64 * GEMM_BK * 2;        // 64 x 64 bf16, 8 KB
+constexpr int PG_A_BYTES = 2 * PG_ATOM;          // a CTA's 128 rows of A; as much of B
+constexpr int PG_STAGE_BYTES = 2 * PG_A_BYTES;
+constexpr int PG_SLOTS = 2;                      // accumulators in TMEM
+constexpr int PG_TMEM_COLS = 512;
+
+// Shared memory: a ring of operand stages, and per epilogue warp the 4 KB
+// boxes its output leaves through (two where an addend arrives in them ahead of
+// the accumulator; none for the statistics).
+template <int EPI>
 struct PgCfg {
-    static constexpr int ATOM = 64 * GEMM_BK * 2;            // 64 x 64 bf16, 8 KB
-    static constexpr int A_BYTES = 2 * ATOM, B_BYTES = 2 * ATOM;
-    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES = 6;
-    static constexpr int SLOTS = 2;
-    static constexpr int TMEM_COLS = 512;
-    static constexpr int STAGING = 2 * 4 * 4096;             // two 4 KB buffers per epilogue warp
-    static constexpr int NBARS = 2 * STAGES + 2 * SLOTS + 1;
-    static constexpr int SMEM = STAGES * STAGE_BYTES + STAGING + 1024 /*align*/ + NBARS * 8 + 16;
+    static constexpr int BUFS = EPI == PG_STATS ? 0 : EPI == PG_BF16_ADD ? 2 : 1;
+    static constexpr int STAGES = 7 - BUFS;
+    static constexpr int STAGING = BUFS * PG_EPI_WARPS * 4096;
+    static constexpr int NBARS = 2 * STAGES + 2 * PG_SLOTS + 1 + PG_EPI_WARPS;
+    static constexpr int SMEM = STAGES * PG_STAGE_BYTES + STAGING + 1024 /*align*/ + NBARS * 8 + 16;
     static_assert(SMEM <= 232448, "more than 227 KB of shared memory");
 };
 
@@ -61,10 +76,12 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// One unit of work: a tile and its K blocks (the same range of every segment).
+// One unit of work: a tile and its K blocks (the same range of every segment),
+// in parts of at most p.part_blocks blocks per segment.
 struct Unit {
     int m0, n0, nt, split;
     int k0, k1;              // blocks of each segment
+    int parts;
 };
 
 struct Shape {
@@ -97,111 +114,108 @@ __device__ __forceinline__ Unit unit_of(const PairGemmParams &p, const Shape &sh
     t.n0 = t.nt * PG_BN;
     t.k0 = (int)((long long)sh.kblocks * t.split / p.splits);
     t.k1 = (int)((long long)sh.kblocks * (t.split + 1) / p.splits);
+    t.parts = (t.k1 - t.k0 + p.part_blocks - 1) / p.part_blocks;
     return t;
 }
 
-// This warp's 32 rows x 128 bytes (lane = row, eight 16-byte pieces in v) to
-// the output map, through one of the warp's two staging buffers.  Boxes
-// outside the map are skipped; TMA clips those that cross its edge.
-template <bool ADD>
-__device__ __forceinline__ void store_box(const PairGemmParams &p, uint8_t *stage2, int &buf, const uint4 (&v)[8],
-                                          int lane, int col, int row)
+// Writes 128 bytes of each of this warp's 32 rows (lane = row, eight 16-byte
+// pieces in v) into a staging box, as the 128-byte swizzle lays them out.
+__device__ __forceinline__ void fill_box(uint8_t *box, const uint4 (&v)[8], int lane)
 {
-    uint8_t *stage = stage2 + buf * 4096;
-    if (lane == 0)
-        bulk_wait_group_read<1>();              // the store before the last has left this buffer
-    __syncwarp();
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-        *reinterpret_cast<uint4 *>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = v[q];
+        *reinterpret_cast<uint4 *>(box + lane * 128 + ((q ^ (lane & 7)) << 4)) = v[q];
     fence_proxy_async_smem();
     __syncwarp();
+}
+
+// Sends a filled box to the output map.  Boxes outside the map are skipped; TMA
+// clips those that cross its edge.
+template <bool ADD>
+__device__ __forceinline__ void send_box(const PairGemmParams &p, const uint8_t *box, int lane, int col, int row)
+{
     if (lane == 0) {
         if (col < p.out_cols && row < p.out_rows) {
             if (ADD)
-                tma_reduce_add_2d(&p.tmOut, smem_u32(stage), col, row);
+                tma_reduce_add_2d(&p.tmOut, smem_u32(box), col, row);
             else
-                tma_store_2d(&p.tmOut, smem_u32(stage), col, row);
+                tma_store_2d(&p.tmOut, smem_u32(box), col, row);
         }
         bulk_commit_group();
     }
-    buf ^= 1;
 }
 
-// Softmax statistics of this lane's row over the tile's columns: a base b (in
-// log2) and s = sum 2^(z log2 e - b), 64 columns at a time, s rescaled when a
-// later 64 hold a larger value.  b is finite even when the largest logit is
-// not, so that an infinite or NaN logit shows in s.
-__device__ __forceinline__ void epilogue_stats(const PairGemmParams &p, const Shape &sh, const Unit &t, uint32_t tacc,
-                                               int row)
+// through the warp's only box: free once the store before has read it
+template <bool ADD>
+__device__ __forceinline__ void store_box(const PairGemmParams &p, uint8_t *box, const uint4 (&v)[8], int lane,
+                                          int col, int row)
 {
+    if (lane == 0)
+        bulk_wait_group_read<0>();
+    __syncwarp();
+    fill_box(box, v, lane);
+    send_box<ADD>(p, box, lane, col, row);
+}
+
+// Softmax statistics of this lane's row over the warp's 128 columns: a base b
+// (in log2) and s = sum 2^(z log2 e - b).  b is finite even when the largest
+// logit is not, so that an infinite or NaN logit shows in s.
+__device__ __forceinline__ void epilogue_stats(const PairGemmParams &p, const Shape &sh, const Unit &t,
+                                               uint32_t (&z)[PG_HALF], int half, int row)
+{
+    const int col0 = t.n0 + half * PG_HALF;
+    const int ncols = min(PG_HALF, p.N - col0);
+    if (ncols <= 0)
+        return;
+    if (ncols < PG_HALF)
+#pragma unroll
+        for (int i = 0; i < PG_HALF; ++i)
+            if (i >= ncols)
+                z[i] = 0xff800000u;
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < PG_HALF; ++i)
+        m[i & 3] = fmaxf(m[i & 3], __uint_as_float(z[i]));
+    float base = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * LOG2E;
+    if (!(fabsf(base) < INFINITY))
+        base = 0.0f;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < PG_HALF; ++i)
+        s[i & 3] += ex2_approx(fmaf(__uint_as_float(z[i]), LOG2E, -base));
     const bool valid = row < sh.M;
-    const int rel = valid ? p.target[row] - (p.n0 + t.n0) : -1;
-    const int ncols = min(PG_BN, p.N - t.n0);
-    float b = -INFINITY, s = 0.0f, zt = 0.0f;
-    bool found = false;
-#pragma unroll 1
-    for (int c = 0; c < ncols; c += 64) {
-        uint32_t r[64];
-        tmem_load64(tacc + c, r);
-        if (ncols - c < 64)
+    const int at = valid ? p.target[row] - (p.n0 + col0) : -1;
+    const bool mine = at >= 0 && at < ncols;
+    float zt = 0.0f;
+    if (__any_sync(0xffffffffu, mine)) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-                if (i >= ncols - c)
-                    r[i] = 0xff800000u;
-        float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-            m0 = fmaxf(m0, __uint_as_float(r[i]));
-            m1 = fmaxf(m1, __uint_as_float(r[i + 1]));
-        }
-        float base = fmaxf(b, fmaxf(m0, m1) * LOG2E);
-        if (!(fabsf(base) < INFINITY))
-            base = 0.0f;
-        float s0 = s * ex2_approx(b - base), s1 = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-            s0 += ex2_approx(fmaf(__uint_as_float(r[i]), LOG2E, -base));
-            s1 += ex2_approx(fmaf(__uint_as_float(r[i + 1]), LOG2E, -base));
-        }
-        s = s0 + s1;
-        b = base;
-        const int at = rel - c;
-        if (__any_sync(0xffffffffu, at >= 0 && at < 64)) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-                if (at == i) {
-                    zt = __uint_as_float(r[i]);
-                    found = true;
-                }
-        }
+        for (int i = 0; i < PG_HALF; ++i)
+            if (at == i)
+                zt = __uint_as_float(z[i]);
     }
     if (valid) {
-        p.stats[(size_t)t.nt * p.ld_stats + row] = make_float2(b, s);
-        if (found)
+        p.stats[(size_t)(2 * t.nt + half) * p.ld_stats + row] = make_float2(base, (s[0] + s[1]) + (s[2] + s[3]));
+        if (mine)
             p.target_logit[row] = zt;
     }
 }
 
-// dz of the tile in bf16, 64 columns at a time.  The rounding (half a step,
+// dz of the warp's columns in bf16, 64 at a time.  The rounding (half a step,
 // 2^-8 of each value) makes dz an operand of the tensor core; the rows' weights
 // are divided by the largest of them first, so that a mean's equal weights
 // are 1 exactly and add no rounding of their own, common to every value.
 __device__ __forceinline__ void epilogue_dlogits(const PairGemmParams &p, const Shape &sh, const Unit &t,
-                                                 uint32_t tacc, int row, int row0, int lane, uint8_t *stage, int &buf)
+                                                 uint32_t tacc, int half, int row, int row0, int lane, uint8_t *box)
 {
     const bool valid = row < sh.M;
-    const int rel = valid ? p.target[row] - (p.n0 + t.n0) : -1;
     const float nl = valid ? -p.lse[row] * LOG2E : 0.0f;
     const float w = valid ? p.weight[row] : 0.0f;
-    const int ncols = min(PG_BN, p.N - t.n0);
+    const int target = valid ? p.target[row] - p.n0 : -1;
 #pragma unroll 1
-    for (int c = 0; c < PG_BN; c += 64) {
-        if (c >= ncols)
-            break;
+    for (int c = t.n0 + half * PG_HALF; c < min(t.n0 + (half + 1) * PG_HALF, p.N); c += 64) {
         uint32_t r[64];
-        tmem_load64(tacc + c, r);
-        const int at = rel - c;
+        tmem_load64(tacc + (c - t.n0), r);
+        const int at = target - c;
         float f[64];
 #pragma unroll
         for (int i = 0; i < 64; ++i)
@@ -214,92 +228,85 @@ __device__ __forceinline__ void epilogue_dlogits(const PairGemmParams &p, const 
         }
 #pragma unroll
         for (int i = 0; i < 64; ++i)
-            f[i] = valid && i < ncols - c ? f[i] * w : 0.0f;
+            f[i] = valid ? f[i] * w : 0.0f;
+        if (p.N - c < 64)
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+                if (i >= p.N - c)
+                    f[i] = 0.0f;
         uint4 v[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q)
             v[q] = make_uint4(bf16x2(f[8 * q], f[8 * q + 1]), bf16x2(f[8 * q + 2], f[8 * q + 3]),
                               bf16x2(f[8 * q + 4], f[8 * q + 5]), bf16x2(f[8 * q + 6], f[8 * q + 7]));
-        store_box<false>(p, stage, buf, v, lane, t.n0 + c, row0);
+        store_box<false>(p, box, v, lane, c, row0);
     }
 }
 
-// fp32 tile into the split's slice.  Each element is stored or added to once
-// per launch, so the sums' order is that of the launches.
-__device__ __forceinline__ void epilogue_partial(const PairGemmParams &p, const Unit &t, uint32_t tacc, bool empty,
-                                                 int row0, int lane, uint8_t *stage, int &buf)
+// The warp's fp32 sums into the split's slice.  Each element is stored or added
+// to once per launch, so the sums' order is that of the launches.
+__device__ __forceinline__ void epilogue_partial(const PairGemmParams &p, const Unit &t, const uint32_t (&z)[PG_HALF],
+                                                 int half, int row0, int lane, uint8_t *box)
 {
-    const int ncols = min(PG_BN, p.N - t.n0);
-#pragma unroll 1
-    for (int c = 0; c < ncols; c += 32) {
-        uint32_t r[32];
-        if (empty) {
+    const int row = t.split * p.split_rows + row0;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                r[i] = 0u;
-        } else {
-            tmem_load32(tacc + c, r);
+    for (int c = 0; c < PG_HALF; c += 32) {
+        const int col = t.n0 + half * PG_HALF + c;
+        if (col < p.N) {
+            uint4 v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                v[q] = make_uint4(z[c + 4 * q], z[c + 4 * q + 1], z[c + 4 * q + 2], z[c + 4 * q + 3]);
+            if (p.accumulate)
+                store_box<true>(p, box, v, lane, col, row);
+            else
+                store_box<false>(p, box, v, lane, col, row);
         }
-        uint4 v[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-            v[q] = make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
-        const int row = t.split * p.split_rows + row0;
-        if (p.accumulate)
-            store_box<true>(p, stage, buf, v, lane, t.n0 + c, row);
-        else
-            store_box<false>(p, stage, buf, v, lane, t.n0 + c, row);
     }
 }
 
-// bf16 tile, scaled, with an optional bf16 addend; one rounding.
-__device__ __forceinline__ void epilogue_bf16(const PairGemmParams &p, const Unit &t, uint32_t tacc, bool empty,
-                                              int row, int row0, int lane, uint8_t *stage, int &buf)
+// One 64-column box of a bf16 output, scaled, plus the addend that lies in the
+// box (as TMA laid it out there) if there is one; one rounding.
+template <bool ADD>
+__device__ __forceinline__ void bf16_box(uint32_t tacc, bool empty, float scale, const uint8_t *box, int lane,
+                                         uint4 (&v)[8])
 {
-    const int ncols = min(PG_BN, p.N - t.n0);
-    const float scale = p.meta ? p.meta->scale : 1.0f;
-    const bool has_add = p.add && row < p.out_rows;
-#pragma unroll 1
-    for (int c = 0; c < ncols; c += 64) {
-        uint32_t r[64];
-        if (empty) {
+    uint32_t r[64];
+    if (empty) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-                r[i] = 0u;
-        } else {
-            tmem_load64(tacc + c, r);
-        }
-        uint4 v[8];
+        for (int i = 0; i < 64; ++i)
+            r[i] = 0u;
+    } else {
+        tmem_load64(tacc, r);
+    }
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            float f[8];
+    for (int q = 0; q < 8; ++q) {
+        float f[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                f[i] = __uint_as_float(r[8 * q + i]) * scale;
-            if (has_add && c + 8 * q < ncols) {           // (N is a multiple of 8)
-                const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p.add + (size_t)row * p.N + t.n0 + c + 8 * q));
-                const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+        for (int i = 0; i < 8; ++i)
+            f[i] = __uint_as_float(r[8 * q + i]) * scale;
+        if (ADD) {
+            const uint4 a = *reinterpret_cast<const uint4 *>(box + lane * 128 + ((q ^ (lane & 7)) << 4));
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    f[2 * i] += __uint_as_float(w[i] << 16);
-                    f[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
-                }
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] += __uint_as_float(w[i] << 16);
+                f[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
             }
-            v[q] = make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]), bf16x2(f[6], f[7]));
         }
-        store_box<false>(p, stage, buf, v, lane, t.n0 + c, row0 + p.out_row0);
+        v[q] = make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]), bf16x2(f[6], f[7]));
     }
 }
 
 template <int EPI, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_constant__ PairGemmParams p)
 {
-    using C = PgCfg;
+    using C = PgCfg<EPI>;
     constexpr uint32_t IDESC = idesc_bf16_f32(PG_BM, PG_BN, A_MN, B_MN);
     extern __shared__ uint8_t dsmem[];
     const uint32_t raw = smem_u32(dsmem);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    uint8_t *staging = dsmem + (base - raw) + C::STAGES * C::STAGE_BYTES;
+    uint8_t *staging = dsmem + (base - raw) + C::STAGES * PG_STAGE_BYTES;
     uint64_t *bars = reinterpret_cast<uint64_t *>(staging + C::STAGING);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + C::NBARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
@@ -312,27 +319,30 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
     auto full_bar = [&](int st) { return bar0 + 8u * st; };
     auto empty_bar = [&](int st) { return bar0 + 8u * (C::STAGES + st); };
     const uint32_t tfull0 = bar0 + 8u * (2 * C::STAGES);
-    const uint32_t tempty0 = tfull0 + 8u * C::SLOTS;
-    const uint32_t fin_bar = tempty0 + 8u * C::SLOTS;
+    const uint32_t tempty0 = tfull0 + 8u * PG_SLOTS;
+    const uint32_t fin_bar = tempty0 + 8u * PG_SLOTS;
+    const uint32_t add_bar0 = fin_bar + 8u;
 
     if (threadIdx.x == 0) {
         for (int st = 0; st < C::STAGES; ++st) {
             mbar_init(full_bar(st), 1);
             mbar_init(empty_bar(st), 1);
         }
-        for (int a = 0; a < C::SLOTS; ++a) {
+        for (int a = 0; a < PG_SLOTS; ++a) {
             mbar_init(tfull0 + 8u * a, 1);
             // this CTA's epilogue warps; the leader's also counts the peer's forwarder
-            mbar_init(tempty0 + 8u * a, 4 + (leader ? 1 : 0));
+            mbar_init(tempty0 + 8u * a, PG_EPI_WARPS + (leader ? 1 : 0));
         }
         mbar_init(fin_bar, 1);
+        for (int w = 0; w < PG_EPI_WARPS; ++w)
+            mbar_init(add_bar0 + 8u * w, 1);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_map(&p.tmA);
         tma_prefetch_map(&p.tmB);
     }
     if (warp == 1) {
-        tmem_alloc_pair(smem_u32(tmem_holder), C::TMEM_COLS);
+        tmem_alloc_pair(smem_u32(tmem_holder), PG_TMEM_COLS);
         tmem_relinquish_pair();
     }
     tc_fence_before();
@@ -359,36 +369,39 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
             for (int u = pair; ok && u < sh.units; u += npairs) {
                 const Unit t = unit_of(p, sh, u);
                 const int m = t.m0 + rank * 128, n = t.n0 + rank * 128;
-                for (int seg = 0; ok && seg < p.nseg; ++seg) {
-                    for (int kb = t.k0; kb < t.k1; ++kb) {
-                        if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t sA = base + stage * C::STAGE_BYTES, sB = sA + C::A_BYTES;
-                        if (leader)
-                            mbar_arrive_expect_tx(full_bar(stage), 2 * C::STAGE_BYTES);
-                        const uint32_t fb = full_leader0 + 8u * stage;
-                        const int k = kb * GEMM_BK;
-                        if (A_MN) {
+                for (int part = 0; part < t.parts; ++part) {
+                    const int kp = t.k0 + part * p.part_blocks, ke = min(kp + p.part_blocks, t.k1);
+                    for (int seg = 0; ok && seg < p.nseg; ++seg) {
+                        for (int kb = kp; kb < ke; ++kb) {
+                            if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) {
+                                ok = false;
+                                break;
+                            }
+                            const uint32_t sA = base + stage * PG_STAGE_BYTES, sB = sA + PG_A_BYTES;
+                            if (leader)
+                                mbar_arrive_expect_tx(full_bar(stage), 2 * PG_STAGE_BYTES);
+                            const uint32_t fb = full_leader0 + 8u * stage;
+                            const int k = kb * GEMM_BK;
+                            if (A_MN) {
 #pragma unroll
-                            for (int q = 0; q < 2; ++q)
-                                tma_load_2d_pair(sA + q * C::ATOM, ma, fb, m + q * 64, k + p.a_off[seg]);
-                        } else {
-                            tma_load_2d_pair(sA, ma, fb, k, m + p.a_off[seg]);
-                        }
-                        if (B_MN) {
+                                for (int q = 0; q < 2; ++q)
+                                    tma_load_2d_pair(sA + q * PG_ATOM, ma, fb, m + q * 64, k + p.a_off[seg]);
+                            } else {
+                                tma_load_2d_pair(sA, ma, fb, k, m + p.a_off[seg]);
+                            }
+                            if (B_MN) {
 #pragma unroll
-                            for (int q = 0; q < 2; ++q)
-                                tma_load_2d_pair(sB + q * C::ATOM, mb, fb, n + q * 64, k + p.b_off[seg]);
-                        } else {
-                            tma_load_2d_pair(sB, mb, fb, k, n + p.b_off[seg]);
-                        }
-                        issued |= 1u << stage;
-                        issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-                        if (++stage == C::STAGES) {
-                            stage = 0;
-                            phase ^= 1u;
+                                for (int q = 0; q < 2; ++q)
+                                    tma_load_2d_pair(sB + q * PG_ATOM, mb, fb, n + q * 64, k + p.b_off[seg]);
+                            } else {
+                                tma_load_2d_pair(sB, mb, fb, k, n + p.b_off[seg]);
+                            }
+                            issued |= 1u << stage;
+                            issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+                            if (++stage == C::STAGES) {
+                                stage = 0;
+                                phase ^= 1u;
+                            }
                         }
                     }
                 }
@@ -411,40 +424,43 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
             bool ok = true;
             for (int u = pair; ok && u < sh.units; u += npairs) {
                 const Unit t = unit_of(p, sh, u);
-                const int nkb = (t.k1 - t.k0) * p.nseg;
-                if (nkb == 0)
-                    continue;
-                const uint32_t slot = ctr % C::SLOTS, par = (ctr / C::SLOTS) & 1u;
-                // (the peer's forwarder arrives here across the pair)
-                if (!mbar_wait_cluster(tempty0 + 8u * slot, par ^ 1u, abort_flag))
-                    break;
-                tc_fence_after();
-                const uint32_t d = tmem + slot * 256;
-                for (int kb = 0; kb < nkb; ++kb) {
-                    if (!mbar_wait(full_bar(stage), phase, abort_flag)) {
+                for (int part = 0; ok && part < t.parts; ++part) {
+                    const int kp = t.k0 + part * p.part_blocks, ke = min(kp + p.part_blocks, t.k1);
+                    const int nkb = (ke - kp) * p.nseg;
+                    const uint32_t slot = ctr % PG_SLOTS, par = (ctr / PG_SLOTS) & 1u;
+                    // (the peer's forwarder arrives here across the pair)
+                    if (!mbar_wait_cluster(tempty0 + 8u * slot, par ^ 1u, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sA = base + stage * C::STAGE_BYTES, sB = sA + C::A_BYTES;
+                    const uint32_t d = tmem + slot * 256;
+                    for (int kb = 0; kb < nkb; ++kb) {
+                        if (!mbar_wait(full_bar(stage), phase, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sA = base + stage * PG_STAGE_BYTES, sB = sA + PG_A_BYTES;
 #pragma unroll
-                    for (int kk = 0; kk < GEMM_BK / 16; ++kk)
-                        // 16 K: 32 B along a K-major row, 2048 B (two 8-row atoms) of an MN-major operand
-                        umma_bf16_pair(d,
-                                       A_MN ? sdesc_mnmajor_sw128(sA + kk * 2048, C::ATOM)
-                                            : sdesc_kmajor_sw128(sA + kk * 32),
-                                       B_MN ? sdesc_mnmajor_sw128(sB + kk * 2048, C::ATOM)
-                                            : sdesc_kmajor_sw128(sB + kk * 32),
-                                       IDESC, (kb > 0 || kk > 0) ? 1u : 0u);
-                    umma_commit_pair(empty_bar(stage), 0x3);          // both CTAs' stage is read
-                    if (++stage == C::STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
+                        for (int kk = 0; kk < GEMM_BK / 16; ++kk)
+                            // 16 K: 32 B along a K-major row, 2048 B (two 8-row atoms) of an MN-major operand
+                            umma_bf16_pair(d,
+                                           A_MN ? sdesc_mnmajor_sw128(sA + kk * 2048, PG_ATOM)
+                                                : sdesc_kmajor_sw128(sA + kk * 32),
+                                           B_MN ? sdesc_mnmajor_sw128(sB + kk * 2048, PG_ATOM)
+                                                : sdesc_kmajor_sw128(sB + kk * 32),
+                                           IDESC, (kb > 0 || kk > 0) ? 1u : 0u);
+                        umma_commit_pair(empty_bar(stage), 0x3);      // both CTAs' stage is read
+                        if (++stage == C::STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
-                }
-                if (ok) {
-                    umma_commit_pair(tfull0 + 8u * slot, 0x3);        // accumulator ready in both TMEMs
-                    ++ctr;
+                    if (ok) {
+                        umma_commit_pair(tfull0 + 8u * slot, 0x3);    // accumulator ready in both TMEMs
+                        ++ctr;
+                    }
                 }
             }
             umma_commit_pair(fin_bar, 0x1);
@@ -453,57 +469,145 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
             // ------------------------------------------- the peer's forwarder
             const uint32_t tempty_leader = mapa_shared(tempty0, 0);
             uint32_t ctr = 0;
-            for (int u = pair; u < sh.units; u += npairs) {
+            bool ok = true;
+            for (int u = pair; ok && u < sh.units; u += npairs) {
                 const Unit t = unit_of(p, sh, u);
-                if (t.k0 == t.k1)
-                    continue;
-                const uint32_t slot = ctr % C::SLOTS, par = (ctr / C::SLOTS) & 1u;
-                if (!mbar_wait(tempty0 + 8u * slot, par, abort_flag))
-                    break;
-                mbar_arrive_cluster(tempty_leader + 8u * slot);
-                ++ctr;
+                for (int part = 0; part < t.parts; ++part, ++ctr) {
+                    const uint32_t slot = ctr % PG_SLOTS, par = (ctr / PG_SLOTS) & 1u;
+                    if (!mbar_wait(tempty0 + 8u * slot, par, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_cluster(tempty_leader + 8u * slot);
+                }
             }
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        const int quad = warp & 3;
-        uint8_t *stage = staging + (warp - 2) * (2 * 4096);
-        int buf = 0;
-        uint32_t ctr = 0;
-        for (int u = pair; u < sh.units; u += npairs) {
+        const int ew = warp - 2, quad = warp & 3, half = ew >> 2;
+        uint8_t *boxes = staging + ew * (C::BUFS * 4096);
+        const uint32_t add_bar = add_bar0 + 8u * ew;
+        const float scale = (EPI == PG_BF16 && p.meta) ? p.meta->scale : 1.0f;
+        uint32_t ctr = 0, add_phase = 0;
+        bool ok = true, add_pending = false;
+        // waits for the next accumulator (the whole warp gets the answer)
+        auto accumulator = [&]() {
+            int got = 1;
+            if (lane == 0)
+                got = mbar_wait(tfull0 + 8u * (ctr % PG_SLOTS), (ctr / PG_SLOTS) & 1u, abort_flag) ? 1 : 0;
+            got = __shfl_sync(0xffffffffu, got, 0);
+            __syncwarp();
+            tc_fence_after();
+            return got != 0;
+        };
+        auto tacc = [&]() {
+            return tmem + ((uint32_t)(quad * 32) << 16) + (ctr % PG_SLOTS) * 256 + half * PG_HALF;
+        };
+        // gives the accumulator back (the peer's forwarder passes it on to the leader)
+        auto release = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(tempty0 + 8u * (ctr % PG_SLOTS));
+            ++ctr;
+        };
+        for (int u = pair; ok && u < sh.units; u += npairs) {
             const Unit t = unit_of(p, sh, u);
-            const bool empty = t.k0 == t.k1;
-            const uint32_t slot = ctr % C::SLOTS, par = (ctr / C::SLOTS) & 1u;
-            if (!empty) {
-                int ok = 1;
-                if (lane == 0)
-                    ok = mbar_wait(tfull0 + 8u * slot, par, abort_flag) ? 1 : 0;
-                ok = __shfl_sync(0xffffffffu, ok, 0);
+            const int row0 = t.m0 + rank * 128 + quad * 32, col0 = t.n0 + half * PG_HALF;
+            if constexpr (EPI == PG_STATS || EPI == PG_PARTIAL) {
+                uint32_t z[PG_HALF];
+                if (t.parts == 0) {
+#pragma unroll
+                    for (int i = 0; i < PG_HALF; ++i)
+                        z[i] = 0u;
+                }
+                for (int part = 0; part < t.parts; ++part) {
+                    if (!accumulator()) {
+                        ok = false;
+                        break;
+                    }
+                    if (part == 0) {
+#pragma unroll
+                        for (int c = 0; c < PG_HALF; c += 32)
+                            tmem_load32(tacc() + c, z + c);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < PG_HALF; c += 32) {
+                            uint32_t r[32];
+                            tmem_load32(tacc() + c, r);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                z[c + i] = __float_as_uint(__uint_as_float(z[c + i]) + __uint_as_float(r[i]));
+                        }
+                    }
+                    release();
+                }
                 if (!ok)
                     break;
-                __syncwarp();
-                tc_fence_after();
-            }
-            const uint32_t tacc = tmem + ((uint32_t)(quad * 32) << 16) + slot * 256;
-            const int row0 = t.m0 + rank * 128 + quad * 32;
-            if (EPI == PG_STATS)
-                epilogue_stats(p, sh, t, tacc, row0 + lane);
-            else if (EPI == PG_DLOGITS)
-                epilogue_dlogits(p, sh, t, tacc, row0 + lane, row0, lane, stage, buf);
-            else if (EPI == PG_PARTIAL)
-                epilogue_partial(p, t, tacc, empty, row0, lane, stage, buf);
-            else
-                epilogue_bf16(p, t, tacc, empty, row0 + lane, row0, lane, stage, buf);
-            if (!empty) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(tempty0 + 8u * slot);   // (the peer's forwarder passes it on to the leader)
-                ++ctr;
+                if constexpr (EPI == PG_STATS)
+                    epilogue_stats(p, sh, t, z, half, row0 + lane);
+                else
+                    epilogue_partial(p, t, z, half, row0, lane, boxes);
+            } else {
+                // (one part: the accumulator's values are used as they are)
+                const bool empty = t.parts == 0;
+                if constexpr (EPI == PG_BF16_ADD) {
+                    // the addend's two boxes, ahead of the accumulator
+                    if (lane == 0) {
+                        bulk_wait_group_read<0>();
+                        mbar_arrive_expect_tx(add_bar, 2 * 4096);
+                        tma_load_2d(smem_u32(boxes), &p.tmHidden, add_bar, col0, row0);
+                        tma_load_2d(smem_u32(boxes + 4096), &p.tmHidden, add_bar, col0 + 64, row0);
+                        add_pending = true;
+                    }
+                }
+                if (!empty && !accumulator()) {
+                    ok = false;
+                    break;
+                }
+                if constexpr (EPI == PG_BF16_ADD) {
+                    int got = 1;
+                    if (lane == 0) {
+                        got = mbar_wait(add_bar, add_phase, abort_flag) ? 1 : 0;
+                        add_pending = got == 0;
+                    }
+                    got = __shfl_sync(0xffffffffu, got, 0);
+                    __syncwarp();
+                    if (!got) {
+                        ok = false;
+                        break;
+                    }
+                    add_phase ^= 1u;
+                    uint4 v[2][8];
+                    bf16_box<true>(tacc(), empty, 1.0f, boxes, lane, v[0]);
+                    bf16_box<true>(tacc() + 64, empty, 1.0f, boxes + 4096, lane, v[1]);
+                    if (!empty)
+                        release();
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        fill_box(boxes + 4096 * i, v[i], lane);
+                        send_box<false>(p, boxes + 4096 * i, lane, col0 + 64 * i, row0 + p.out_row0);
+                    }
+                } else if constexpr (EPI == PG_BF16) {
+                    uint4 v[2][8];
+                    bf16_box<false>(tacc(), empty, scale, nullptr, lane, v[0]);
+                    bf16_box<false>(tacc() + 64, empty, scale, nullptr, lane, v[1]);
+                    if (!empty)
+                        release();
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        store_box<false>(p, boxes, v[i], lane, col0 + 64 * i, row0 + p.out_row0);
+                } else {
+                    epilogue_dlogits(p, sh, t, tacc() - half * PG_HALF, half, row0 + lane, row0, lane, boxes);
+                    release();
+                }
             }
         }
-        if (lane == 0)
+        if (lane == 0) {
+            if (EPI == PG_BF16_ADD && add_pending)
+                mbar_drain(add_bar, add_phase);
             bulk_wait_group_all();              // this warp's output stores have completed
+        }
     }
 
     __syncwarp();
@@ -517,7 +621,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
     cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem, C::TMEM_COLS);
+        tmem_dealloc_pair(tmem, PG_TMEM_COLS);
     }
     if (threadIdx.x == 0 && *abort_flag && p.status)
         atomicOr(p.status, ST_TIMEOUT);
@@ -540,12 +644,12 @@ cudaError_t launch_one(const PairGemmParams &p, int max_units, cudaStream_t s)
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.blockDim = dim3(PG_THREADS);
-    cfg.dynamicSmemBytes = PgCfg::SMEM;
+    cfg.dynamicSmemBytes = PgCfg<EPI>::SMEM;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     if (configured_device != dev) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PgCfg::SMEM);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PgCfg<EPI>::SMEM);
         if (e != cudaSuccess)
             return e;
         cfg.gridDim = dim3(2);
@@ -579,6 +683,8 @@ cudaError_t launch_pair_gemm(PairEpilogue epi, bool a_mn, bool b_mn, const PairG
         return launch_one<PG_PARTIAL, true, true>(p, max_units, s);
     if (epi == PG_BF16 && !a_mn && b_mn)
         return launch_one<PG_BF16, false, true>(p, max_units, s);
+    if (epi == PG_BF16_ADD && !a_mn && b_mn)
+        return launch_one<PG_BF16_ADD, false, true>(p, max_units, s);
     if (epi == PG_BF16 && a_mn && b_mn)
         return launch_one<PG_BF16, true, true>(p, max_units, s);
     return cudaErrorInvalidValue;

@@ -6,7 +6,8 @@
 // w_j = rsf s_j / D, so  ds_j = rsf / D (dw_j - sum_i dw_i s_i / D).  The balance
 // loss E sum_e f_e mean_t(s_te / Z_t), Z_t = sum_e s_te, f_e = counts_e / (k T)
 // fixed, adds  ds_e += d_aux E / T (f_e - sum_e' f_e' s_e' / Z) / Z.  Then
-// dL = ds s (1 - s), with 1 - s as sigmoid(-L), which keeps its digits near s = 1.
+// dL = ds s (1 - s), with 1 - s formed as exp(-L) s where L > 0, which keeps its
+// digits near s = 1.
 //
 // dL is written as three bf16 parts (high, middle, low: 24 bits, as the router
 // weight is split for the forward), so that the products with the bf16 hidden
@@ -27,6 +28,15 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
+// sum of the K parts of one logit, in part order
+__device__ __forceinline__ float logit_at(const float *logits, int nparts, long long stride, size_t at)
+{
+    float v = logits[at];
+    for (int q = 1; q < nparts; ++q)
+        v += logits[at + q * stride];
+    return v;
+}
+
 __device__ __forceinline__ uint16_t bf16_bits(float v)
 {
     const __nv_bfloat16 b = __float2bfloat16_rn(v);
@@ -37,7 +47,7 @@ __device__ __forceinline__ uint16_t bf16_bits(float v)
 
 // One warp per token; a lane holds EPL = E / 32 neighbouring experts.
 template <int EPL>
-__global__ void __launch_bounds__(256) route_grad_kernel(const float *__restrict__ logits,
+__global__ void __launch_bounds__(256) route_grad_kernel(const float *__restrict__ logits, int nparts,
                                                          const int32_t *__restrict__ idx,
                                                          const float *__restrict__ d_w,
                                                          const int32_t *__restrict__ counts,
@@ -48,6 +58,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const float *__restrict
     pdl_wait();
     const int lane = threadIdx.x & 31;
     const int warps = gridDim.x * (blockDim.x >> 5);
+    const long long stride = (long long)T * E;
     float f[EPL];
     const float aux = d_aux ? *d_aux * ((float)E / (float)T) : 0.0f;
 #pragma unroll
@@ -61,6 +72,12 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const float *__restrict
             const float4 q = *reinterpret_cast<const float4 *>(row + lane * EPL + i);
             L[i] = q.x; L[i + 1] = q.y; L[i + 2] = q.z; L[i + 3] = q.w;
         }
+        for (int part = 1; part < nparts; ++part)
+#pragma unroll
+            for (int i = 0; i < EPL; i += 4) {
+                const float4 q = *reinterpret_cast<const float4 *>(row + part * stride + lane * EPL + i);
+                L[i] += q.x; L[i + 1] += q.y; L[i + 2] += q.z; L[i + 3] += q.w;
+            }
         // lane j < k: the chosen expert j
         int e = -1;
         float dw = 0.0f, sj = 0.0f;
@@ -71,7 +88,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const float *__restrict
                 e = -1;
             } else {
                 dw = d_w[(size_t)t * k + lane];
-                sj = router_sigmoid(row[e]);
+                sj = router_sigmoid(logit_at(row, nparts, stride, e));
             }
         }
         const float D = warp_sum(sj) + eps;
@@ -109,7 +126,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const float *__restrict
         uint16_t h[3][EPL];
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            float v = ds[i] * s[i] * router_sigmoid(-L[i]);
+            float v = ds[i] * s[i] * (L[i] > 0.0f ? s[i] * __expf(-L[i]) : 1.0f - s[i]);
 #pragma unroll
             for (int q = 0; q < 3; ++q) {
                 h[q][i] = bf16_bits(v);
@@ -147,15 +164,15 @@ __global__ void __launch_bounds__(256) sum_splits_kernel(const float *__restrict
     reinterpret_cast<float4 *>(out)[i] = a;
 }
 
-cudaError_t launch_route_grad(const float *logits, const int32_t *idx, const float *d_w, const int32_t *counts,
+cudaError_t launch_route_grad(const float *logits, int nparts, const int32_t *idx, const float *d_w, const int32_t *counts,
                               const float *d_aux, int T, int E, int k, float rsf, float eps, uint16_t *parts,
                               int *status, cudaStream_t s)
 {
     const int want = (T + 7) / 8, most = 152 * 8;
     const dim3 grid(want < most ? want : most);
-    const cudaError_t e = E == 256 ? launch_pdl(route_grad_kernel<8>, grid, dim3(256), 0, s, logits, idx, d_w, counts,
+    const cudaError_t e = E == 256 ? launch_pdl(route_grad_kernel<8>, grid, dim3(256), 0, s, logits, nparts, idx, d_w, counts,
                                                 d_aux, T, k, rsf, eps, parts, status)
-                                   : launch_pdl(route_grad_kernel<4>, grid, dim3(256), 0, s, logits, idx, d_w, counts,
+                                   : launch_pdl(route_grad_kernel<4>, grid, dim3(256), 0, s, logits, nparts, idx, d_w, counts,
                                                 d_aux, T, k, rsf, eps, parts, status);
     return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
