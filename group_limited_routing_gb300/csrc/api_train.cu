@@ -31,20 +31,18 @@ constexpr int NORM_SMS = 152;
 
 struct NormLayout {
     size_t part_a, part_b, total;
-    int blocks, cpg;
+    BlockNormPlan plan;
 };
 
 NormLayout norm_layout(int T, int H, int groups)
 {
     NormLayout L;
-    L.blocks = block_norm_blocks(T, H, NORM_SMS);
-    L.cpg = block_norm_cpg(T, groups, L.blocks);
+    L.plan = block_norm_plan(T, H, groups, NORM_SMS);
     L.part_a = sizeof(WsHeader);
-    L.part_b = L.part_a + align_up(sizeof(float) * (size_t)groups * L.cpg * H, 256);
-    L.total = L.part_b + align_up(sizeof(float) * (size_t)L.blocks * H, 256);
+    L.part_b = L.part_a + align_up(sizeof(float) * (size_t)groups * L.plan.cpg * H, 256);
+    L.total = L.part_b + align_up(sizeof(float) * (size_t)L.plan.blocks * H, 256);
     return L;
 }
-
 
 // ------------------------------------------------------------ dense products
 constexpr int PAIRS = 76;     // CTA pairs of a full GB300
@@ -246,7 +244,7 @@ int moe_block_norm_backward(int32_t T, int32_t H, int32_t groups, int32_t stream
     p.H = H;
     p.groups = groups;
     p.rows_per_gate = T / groups;
-    p.cpg = L.cpg;
+    p.cpg = L.plan.cpg;
     p.alpha = alpha;
     p.eps = eps;
     p.x = x;
@@ -265,9 +263,9 @@ int moe_block_norm_backward(int32_t T, int32_t H, int32_t groups, int32_t stream
     p.dw_pre = dw_pre;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     int launches = 0;
-    GLR_LAUNCH(KID_BLOCK_NORM_BWD, launch_block_norm_backward(p, stream_f32 != 0, L.blocks, s));
+    GLR_LAUNCH(KID_BLOCK_NORM_BWD, launch_block_norm_backward(p, stream_f32 != 0, L.plan.blocks, s));
     if (d_gate || dw_post || dw_pre)
-        GLR_LAUNCH(KID_BLOCK_NORM_BWD, launch_block_norm_finish(p, L.blocks, s));
+        GLR_LAUNCH(KID_BLOCK_NORM_BWD, launch_block_norm_finish(p, L.plan.blocks, s));
     set_last_launches(launches);
     return MOE_OK;
 }

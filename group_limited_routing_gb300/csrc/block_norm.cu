@@ -16,14 +16,20 @@
 // x and y are read again and r, u, q formed again: reading them costs what
 // reading saved statistics and r would, and the forward need not keep anything.
 //
-// Bound by memory: forward 2 reads + 2 writes of [T, H], backward 4 + 2.  One
-// block holds one row, up to sixteen columns per thread, so a row's values stay
-// in registers and shared memory between the two reductions that it needs.
-// Each thread copies the bytes that it will read itself, rows ahead, into
-// shared memory of its own (cp.async): the loads in flight do not cost
-// registers, and no thread waits for another's copies.  The arithmetic runs on
-// pairs of fp32 values (f32x2): one value at a time, the instructions issued
-// take as long as the memory.
+// Bound by memory: forward 2 reads + 2 writes of [T, H], backward 4 + 2; what
+// decides how near they come is the instructions per column and the loads in
+// flight.  Each thread copies the bytes that it will read itself into shared
+// memory of its own (cp.async), so loads in flight cost no registers and no
+// thread waits for another's copies, and the arithmetic runs on pairs of fp32
+// values (f32x2).
+//   Forward: a row belongs to one warp up to H = 2048 (two up to 4096, four
+//   above), so that 64 columns per lane share each reduction; a row's piece is
+//   fetched for the next row as soon as it has been read.
+//   Backward: a row belongs to a block, 16 columns per thread, because the
+//   column sums of all its rows stay in the threads' registers; rows are
+//   fetched three (fp32 stream: two) ahead.  One warp per row with 64 columns
+//   per lane measured slower (194 against 148 us at T = 32768, H = 2048): its
+//   column sums leave registers for eight warps per SM.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -33,7 +39,8 @@ namespace glr {
 
 namespace {
 
-constexpr int BN_MAX_WARPS = 16;
+constexpr int BN_WARPS = 8;          // forward: warps of a block, 8 / W rows at a time
+constexpr int BN_BWD_WARPS = 16;     // backward: warps of a row at most
 
 // two fp32 values in one register pair
 struct F2 {
@@ -101,9 +108,12 @@ __device__ __forceinline__ void cp_async_wait()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Eight consecutive values of a row: 16 bytes of bf16 or 32 of fp32.  In shared
-// memory the 16-byte pieces of the block's threads lie side by side.
+// Eight consecutive values of a row: 16 bytes of bf16 or 32 of fp32, in 16-byte
+// pieces.  In shared memory the pieces of the block's threads lie side by side.
+constexpr int BN_THREADS = 32 * BN_WARPS;
+
 template <bool F32>
 struct Vec8;
 
@@ -136,11 +146,42 @@ struct Vec8<true> {
     }
 };
 
+// the W warps of a row meet
+template <int W>
+__device__ __forceinline__ void row_barrier(int group)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * W) : "memory");
+}
+
+// Sum over a row's warps, the same bits in every thread (a butterfly, then the
+// warps' sums in warp order).  `slot` alternates between calls, so one barrier
+// per call suffices: a slot is written again only after the barrier of the call
+// between, which every reader of it has passed.
+template <int W>
+__device__ __forceinline__ float row_sum(float v, float (*sm)[BN_WARPS], int &slot)
+{
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (W == 1)
+        return v;
+    const int warp = threadIdx.x >> 5, group = warp / W;
+    if ((threadIdx.x & 31) == 0)
+        sm[slot][warp] = v;
+    row_barrier<W>(group);
+    v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+        v += sm[slot][group * W + w];
+    slot ^= 1;
+    return v;
+}
+
 // Sums over the block, the same bits in every thread (warp sums by butterfly,
 // then the warps' sums in warp order).  `slot` alternates between calls, so one
 // barrier per call suffices: a slot is written again only after the barrier of
 // the call between, which every reader of it has passed.
-__device__ __forceinline__ float block_sum(float v, float (*sm)[BN_MAX_WARPS], int &slot)
+__device__ __forceinline__ float block_sum(float v, float (*sm)[BN_BWD_WARPS], int &slot)
 {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
@@ -161,7 +202,7 @@ __device__ __forceinline__ float block_sum(float v, float (*sm)[BN_MAX_WARPS], i
 // The same for five values.  Each of the first three butterfly steps halves the
 // values a lane carries (lane bits 4, 3, 2 choose which), 9 exchanges in all
 // instead of 25.
-__device__ __forceinline__ void block_sums5(float *t, float (*sm)[BN_MAX_WARPS][8], int &slot)
+__device__ __forceinline__ void block_sums5(float *t, float (*sm)[BN_BWD_WARPS][8], int &slot)
 {
     const int lane = threadIdx.x & 31;
     float a[4];
@@ -200,7 +241,7 @@ __device__ __forceinline__ void block_sums5(float *t, float (*sm)[BN_MAX_WARPS][
     slot ^= 1;
 }
 
-// eight weights (NULL: 1)
+// eight fp32 weights, from shared or global memory (NULL: 1)
 __device__ __forceinline__ void load_vec(const float *w, int v, F2 *f)
 {
     if (!w) {
@@ -209,144 +250,160 @@ __device__ __forceinline__ void load_vec(const float *w, int v, F2 *f)
             f[i] = f2(1.0f);
         return;
     }
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(w) + 2 * v);
-    const float4 b = __ldg(reinterpret_cast<const float4 *>(w) + 2 * v + 1);
+    const float4 a = reinterpret_cast<const float4 *>(w)[2 * v];
+    const float4 b = reinterpret_cast<const float4 *>(w)[2 * v + 1];
     f[0] = f2(a.x, a.y); f[1] = f2(a.z, a.w); f[2] = f2(b.x, b.y); f[3] = f2(b.z, b.w);
+}
+
+// gate * w_post for one vector of columns
+__device__ __forceinline__ void load_gw(const float *gate, const float *w_post, int v, F2 *f)
+{
+    F2 w[4];
+    load_vec(gate, v, f);
+    load_vec(w_post, v, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f[i] = mul2(f[i], w[i]);
 }
 
 // gate * w_post for this thread's columns
 template <int VPT>
-__device__ __forceinline__ void load_gw(const BlockNormParams &p, int group, int nv, F2 (*gw)[4])
+__device__ __forceinline__ void load_gw_columns(const BlockNormParams &p, int group, int nv, F2 (*gw)[4])
 {
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const int v = threadIdx.x + k * blockDim.x;
         if (v >= nv)
             continue;
-        F2 g[4], w[4];
-        load_vec(p.gate ? p.gate + (size_t)group * p.H : nullptr, v, g);
-        load_vec(p.w_post, v, w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            gw[k][i] = mul2(g[i], w[i]);
+        load_gw(p.gate ? p.gate + (size_t)group * p.H : nullptr, p.w_post, v, gw[k]);
     }
 }
 
-// 16-byte pieces per thread and vector of one row's inputs, and the rows in
-// flight: what lets four blocks of a 2048-wide row share an SM's shared memory
-// (48 KB each, 32 KB forward)
+// 16-byte pieces per vector of one row's inputs (x, y, backward also d_n, d_r),
+// and the backward's rows in flight: what lets four blocks of a 2048-wide row
+// share an SM's shared memory (48 KB each)
 template <bool F32, bool HAS_Y, bool BWD>
-struct Ring {
+struct Slots {
     static constexpr int X = F32 ? 2 : 1;
-    static constexpr int PIECES = X + (HAS_Y ? 1 : 0) + (BWD ? X + 1 : 0);
-    static constexpr int ROWS = BWD ? (F32 ? 2 : 3) : (F32 ? 3 : 4);
+    static constexpr int AT_Y = X, AT_DN = X + (HAS_Y ? 1 : 0), AT_DR = AT_DN + 1;
+    static constexpr int PIECES = BWD ? AT_DR + X : AT_DN;
+    static constexpr int ROWS = F32 ? 2 : 3;
 };
+
+// The weights' copies in shared memory, behind the rows' slots.
+__device__ __forceinline__ void stage_weights(const BlockNormParams &p, uint4 *after, const float *&w_post,
+                                              const float *&w_pre)
+{
+    w_post = p.w_post;
+    w_pre = p.w_pre;
+    float *post = reinterpret_cast<float *>(after), *pre = post + p.H;
+    for (int h = threadIdx.x; h < p.H; h += BN_THREADS) {
+        if (w_post)
+            post[h] = w_post[h];
+        if (w_pre)
+            pre[h] = w_pre[h];
+    }
+    __syncthreads();
+    w_post = w_post ? post : nullptr;
+    w_pre = w_pre ? pre : nullptr;
+}
 
 }  // namespace
 
-// Rows [b T / grid, (b + 1) T / grid) of block b.
-template <int VPT, bool F32, bool HAS_Y>
-__global__ void __launch_bounds__(512) block_norm_kernel(const BlockNormParams p)
+// Row group g of block b takes rows g grid + b, and every (groups grid)-th after.
+template <int VPT, int W, bool F32, bool HAS_Y>
+__global__ void __launch_bounds__(BN_THREADS) block_norm_kernel(const BlockNormParams p)
 {
     using X = Vec8<F32>;
-    constexpr int P = Ring<F32, HAS_Y, false>::PIECES, S = Ring<F32, HAS_Y, false>::ROWS;
-    extern __shared__ uint4 ring[];      // [S][VPT][P][threads]
-    __shared__ float sm[2][BN_MAX_WARPS];
+    using S = Slots<F32, HAS_Y, false>;
+    extern __shared__ uint4 dyn[];       // [VPT][PIECES][threads], weights
+    __shared__ float sm[2][BN_WARPS];
     pdl_wait();
-    const int nt = blockDim.x;
     const int nv = p.H / 8;
-    const int row0 = (int)((long long)blockIdx.x * p.T / gridDim.x);
-    const int row1 = (int)((long long)(blockIdx.x + 1) * p.T / gridDim.x);
     const float inv_h = 1.0f / (float)p.H;
     const F2 alpha = f2(p.alpha);
-    int slot = 0, group = -1;
-    uint4 *mine = ring + threadIdx.x;
-    auto fetch = [&](int row, int st) {
-        if (row < row1)
+    const int group = threadIdx.x / (32 * W), lane = threadIdx.x % (32 * W);
+    const int step = (BN_WARPS / W) * gridDim.x;
+    uint4 *mine = dyn + threadIdx.x;
+    const uint32_t mine_s = smem_u32(mine);
+    int slot = 0;
+    auto fetch = [&](int k, int row) {
+        const int v = lane + k * 32 * W;
+        if (row < p.T && v < nv) {
+            const size_t at = (size_t)row * nv + v;
+            const uint32_t dst = mine_s + k * S::PIECES * BN_THREADS * 16;
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int v = threadIdx.x + k * nt;
-                if (v < nv) {
-                    const size_t at = (size_t)row * nv + v;
-                    const uint32_t dst = smem_u32(mine + (st * VPT + k) * P * nt);
-#pragma unroll
-                    for (int i = 0; i < X::PIECES; ++i)
-                        cp_async16(dst + i * nt * 16, static_cast<const uint4 *>(p.x) + at * X::PIECES + i);
-                    if (HAS_Y)
-                        cp_async16(dst + X::PIECES * nt * 16, reinterpret_cast<const uint4 *>(p.y) + at);
-                }
-            }
-        cp_async_commit();
-    };
-#pragma unroll
-    for (int st = 0; st < S; ++st)
-        fetch(row0 + st, st);
-    F2 gw[VPT][4], wpre[VPT][4];
-#pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-        const int v = threadIdx.x + k * nt;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            gw[k][i] = wpre[k][i] = f2(0.0f);
-        if (v < nv)
-            load_vec(p.w_pre, v, wpre[k]);
-    }
-    int st = 0;
-    for (int row = row0; row < row1; ++row) {
-        if (HAS_Y && row / p.rows_per_gate != group) {
-            group = row / p.rows_per_gate;
-            load_gw<VPT>(p, group, nv, gw);
+            for (int i = 0; i < S::X; ++i)
+                cp_async16(dst + i * BN_THREADS * 16, static_cast<const uint4 *>(p.x) + at * S::X + i);
+            if (HAS_Y)
+                cp_async16(dst + S::AT_Y * BN_THREADS * 16, reinterpret_cast<const uint4 *>(p.y) + at);
         }
-        cp_async_wait<S - 1>();
-        F2 r[VPT][4], y[VPT][4];
+    };
+    int row = group * gridDim.x + blockIdx.x;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k)
+        fetch(k, row);
+    const float *w_post, *w_pre;
+    stage_weights(p, dyn + VPT * S::PIECES * BN_THREADS, w_post, w_pre);
+    for (; row < p.T; row += step) {
+        cp_async_wait_all();
+        const float *gate = p.gate ? p.gate + (size_t)(row / p.rows_per_gate) * p.H : nullptr;
+        F2 rho = f2(0.0f);
+        if (HAS_Y) {
+            F2 s = f2(0.0f);
+#pragma unroll
+            for (int k = 0; k < VPT; ++k)
+                if (lane + k * 32 * W < nv) {
+                    F2 y[4];
+                    unpack8(mine[(k * S::PIECES + S::AT_Y) * BN_THREADS], y);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s = fma2(y[i], y[i], s);
+                }
+            rho = f2(rsqrtf(row_sum<W>(sum2(s), sm, slot) * inv_h + p.eps));
+        }
+        F2 r[VPT][4];
         F2 s = f2(0.0f);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                r[k][i] = y[k][i] = f2(0.0f);
-            if (threadIdx.x + k * nt < nv) {
-                const uint4 *at = mine + (st * VPT + k) * P * nt;
-                X::read(at, nt, r[k]);
+            const int v = lane + k * 32 * W;
+            if (v < nv) {
+                const uint4 *at = mine + k * S::PIECES * BN_THREADS;
+                X::read(at, BN_THREADS, r[k]);
                 if (HAS_Y) {
-                    unpack8(at[X::PIECES * nt], y[k]);
+                    F2 y[4], gw[4];
+                    unpack8(at[S::AT_Y * BN_THREADS], y);
+                    load_gw(gate, w_post, v, gw);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        s = fma2(y[k][i], y[k][i], s);
+                        r[k][i] = fma2(alpha, r[k][i], mul2(gw[i], mul2(y[i], rho)));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        r[k][i] = mul2(alpha, r[k][i]);
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s = fma2(r[k][i], r[k][i], s);
+                fetch(k, row + step);
             }
         }
-        fetch(row + S, st);
-        st = st + 1 == S ? 0 : st + 1;
-        F2 rho = f2(0.0f);
-        if (HAS_Y)
-            rho = f2(1.0f / sqrtf(block_sum(sum2(s), sm, slot) * inv_h + p.eps));
-        s = f2(0.0f);
-#pragma unroll
-        for (int k = 0; k < VPT; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                r[k][i] = mul2(alpha, r[k][i]);
-                if (HAS_Y)
-                    r[k][i] = fma2(gw[k][i], mul2(y[k][i], rho), r[k][i]);
-                s = fma2(r[k][i], r[k][i], s);
-            }
-        const F2 sigma = f2(1.0f / sqrtf(block_sum(sum2(s), sm, slot) * inv_h + p.eps));
+        const F2 sigma = f2(rsqrtf(row_sum<W>(sum2(s), sm, slot) * inv_h + p.eps));
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int v = threadIdx.x + k * nt;
-            if (v >= nv)
-                continue;
-            if (p.r)
-                X::store(p.r, (size_t)row * nv + v, r[k]);
-            F2 n[4];
+            const int v = lane + k * 32 * W;
+            if (v < nv) {
+                if (p.r)
+                    X::store(p.r, (size_t)row * nv + v, r[k]);
+                F2 w[4];
+                load_vec(w_pre, v, w);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                n[i] = mul2(mul2(r[k][i], sigma), wpre[k][i]);
-            Vec8<false>::store(p.n, (size_t)row * nv + v, n);
+                for (int i = 0; i < 4; ++i)
+                    w[i] = mul2(mul2(r[k][i], sigma), w[i]);
+                Vec8<false>::store(p.n, (size_t)row * nv + v, w);
+            }
         }
     }
-    cp_async_wait<0>();
 }
 
 // Chunk c holds rows of one gate group only: group c / cpg, its part c % cpg of
@@ -357,11 +414,11 @@ template <int VPT, bool F32, bool HAS_Y>
 __global__ void __launch_bounds__(512) block_norm_backward_kernel(const BlockNormParams p)
 {
     using X = Vec8<F32>;
-    constexpr int P = Ring<F32, HAS_Y, true>::PIECES, S = Ring<F32, HAS_Y, true>::ROWS;
-    constexpr int AT_DN = X::PIECES, AT_DR = X::PIECES + 1, AT_Y = 2 * X::PIECES + 1;
+    using At = Slots<F32, HAS_Y, true>;
+    constexpr int P = At::PIECES, S = At::ROWS, AT_DN = At::AT_DN, AT_DR = At::AT_DR, AT_Y = At::AT_Y;
     extern __shared__ uint4 ring[];      // [S][VPT][P][threads]
-    __shared__ float sm1[2][BN_MAX_WARPS];
-    __shared__ __align__(16) float sm5[2][BN_MAX_WARPS][8];
+    __shared__ float sm1[2][BN_BWD_WARPS];
+    __shared__ __align__(16) float sm5[2][BN_BWD_WARPS][8];
     pdl_wait();
     const int nt = blockDim.x;
     const int nv = p.H / 8;
@@ -417,7 +474,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const BlockNor
     for (int c = c0; c < c1; ++c) {
         const int begin = chunk_begin(c), end = chunk_begin(c + 1);
         if (HAS_Y && (c == c0 || c % p.cpg == 0))
-            load_gw<VPT>(p, c / p.cpg, nv, gw);
+            load_gw_columns<VPT>(p, c / p.cpg, nv, gw);
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
 #pragma unroll
@@ -445,7 +502,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const BlockNor
             }
             float rho = 0.0f;
             if (HAS_Y)
-                rho = 1.0f / sqrtf(block_sum(sum2(s), sm1, slot1) * inv_h + p.eps);
+                rho = rsqrtf(block_sum(sum2(s), sm1, slot1) * inv_h + p.eps);
             // sum r^2, sum dq r, and the three parts of sum du u
             F2 t[5];
 #pragma unroll
@@ -471,14 +528,15 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const BlockNor
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const F2 dq = mul2(dn[i], wpre[k][i]);
-                    r[k][i] = mul2(alpha, r[k][i]);
                     if (HAS_Y) {
                         u[k][i] = mul2(u[k][i], rho2);
                         const F2 a = mul2(gw[k][i], u[k][i]);
-                        r[k][i] = fma2(gw[k][i], u[k][i], r[k][i]);
+                        r[k][i] = fma2(alpha, r[k][i], a);
                         t[2] = fma2(a, dr[i], t[2]);
                         t[3] = fma2(a, dq, t[3]);
                         t[4] = fma2(a, r[k][i], t[4]);
+                    } else {
+                        r[k][i] = mul2(alpha, r[k][i]);
                     }
                     t[0] = fma2(r[k][i], r[k][i], t[0]);
                     t[1] = fma2(dq, r[k][i], t[1]);
@@ -486,7 +544,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const BlockNor
             }
             float q5[5] = {sum2(t[0]), sum2(t[1]), sum2(t[2]), sum2(t[3]), sum2(t[4])};
             block_sums5(q5, sm5, slot5);
-            const float sigma = 1.0f / sqrtf(q5[0] * inv_h + p.eps);
+            const float sigma = rsqrtf(q5[0] * inv_h + p.eps);
             // dr = d_r + sigma dq - (sigma^3 mean(dq r)) r
             const float c_r = sigma * sigma * sigma * (q5[1] * inv_h);
             const float c_u = (q5[2] + sigma * q5[3] - c_r * q5[4]) * inv_h;   // mean(du u)
@@ -541,83 +599,117 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const BlockNor
 
 // The column sums from the chunks' and blocks' partial sums, in a fixed order:
 // dw_pre = sum_b B[b], d_gate[g] = w_post sum_c A[g, c], dw_post = sum_g gate[g]
-// sum_c A[g, c].  32 columns per block, 32 rows of the partial sums at a time.
+// sum_c A[g, c].  A block takes 32 columns: 8 threads of four columns each, 128
+// partial sums at a time, all loads of a thread in flight at once.
 __global__ void __launch_bounds__(1024) block_norm_finish_kernel(const BlockNormParams p, int blocks)
 {
-    __shared__ float sm[32][33];
+    __shared__ float sm[32][32];
     pdl_wait();
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int h = blockIdx.x * 32 + lane;
-    const bool in = h < p.H;
-    auto across = [&](float v) {      // sum over the 32 warps, in warp order; thread (0, lane) gets it
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int col = (lane & 7) * 4, slice = w * 4 + (lane >> 3);
+    const int h = blockIdx.x * 32 + col;
+    const bool in = h < p.H;                      // (H is a multiple of 8)
+    auto add = [](float4 &a, const float4 &b) { a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w; };
+    // sum of partial sums row0 .. row0 + n - 1 by `many` slices, this thread being number `at` of them
+    auto some = [&](const float *part, size_t row0, int n, int at, int many) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = at; i < n; i += many)
+            add(a, *reinterpret_cast<const float4 *>(part + (row0 + i) * p.H + h));
+        return a;
+    };
+    // the warp's four slices, then the 32 warps in order; warp 0 lanes 0..31 get column `lane`
+    auto across = [&](float4 a) {
+#pragma unroll
+        for (int off = 8; off <= 16; off <<= 1) {
+            a.x += __shfl_xor_sync(0xffffffffu, a.x, off);
+            a.y += __shfl_xor_sync(0xffffffffu, a.y, off);
+            a.z += __shfl_xor_sync(0xffffffffu, a.z, off);
+            a.w += __shfl_xor_sync(0xffffffffu, a.w, off);
+        }
         __syncthreads();
-        sm[w][lane] = v;
+        if (lane < 8)
+            *reinterpret_cast<float4 *>(&sm[w][col]) = a;
         __syncthreads();
         float t = 0.0f;
         if (w == 0)
+#pragma unroll
             for (int i = 0; i < 32; ++i)
                 t += sm[i][lane];
         return t;
     };
-    float s = 0.0f;
-#pragma unroll 8
-    for (int b = w; b < blocks; b += 32)
-        if (in)
-            s += p.part_b[(size_t)b * p.H + h];
-    s = across(s);
-    if (w == 0 && in && p.dw_pre)
-        p.dw_pre[h] = s;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int out = blockIdx.x * 32 + lane;       // warp 0's column
+    const bool mine = w == 0 && out < p.H;
+    const float pre = across(in ? some(p.part_b, 0, blocks, slice, 128) : zero);
+    if (mine && p.dw_pre)
+        p.dw_pre[out] = pre;
     if (!p.part_a)
         return;
-    const float wp = (in && p.w_post) ? p.w_post[h] : 1.0f;
-    float post = 0.0f;
-    if (p.cpg == 1) {
-        // whole groups: one per warp and step
-        for (int g = w; g < p.groups; g += 32)
-            if (in) {
-                const float a = p.part_a[(size_t)g * p.H + h];
+    if (p.groups <= 4) {
+        // a few long groups: one after the other, by the whole block
+        const float wp = mine && p.w_post ? p.w_post[out] : 1.0f;
+        float post = 0.0f;
+        for (int g = 0; g < p.groups; ++g) {
+            const float a = across(in ? some(p.part_a, (size_t)g * p.cpg, p.cpg, slice, 128) : zero);
+            if (mine) {
                 if (p.d_gate)
-                    p.d_gate[(size_t)g * p.H + h] = wp * a;
-                post = fmaf(p.gate ? p.gate[(size_t)g * p.H + h] : 1.0f, a, post);
-            }
-    } else {
-        // up to 32 groups at a time, the 32 warps shared out among them
-        const int at_once = min(32, p.groups), wpg = 32 / at_once;
-        const int gi = w / wpg, sub = w % wpg;
-        for (int g0 = 0; g0 < p.groups; g0 += at_once) {
-            const int g = g0 + gi;
-            const bool mine = in && gi < at_once && g < p.groups;
-            float a = 0.0f;
-#pragma unroll 8
-            for (int c = sub; c < p.cpg; c += wpg)
-                if (mine)
-                    a += p.part_a[((size_t)g * p.cpg + c) * p.H + h];
-            __syncthreads();
-            sm[w][lane] = a;
-            __syncthreads();
-            if (mine && sub == 0) {
-                for (int i = 1; i < wpg; ++i)
-                    a += sm[w + i][lane];
-                if (p.d_gate)
-                    p.d_gate[(size_t)g * p.H + h] = wp * a;
-                post = fmaf(p.gate ? p.gate[(size_t)g * p.H + h] : 1.0f, a, post);
+                    p.d_gate[(size_t)g * p.H + out] = wp * a;
+                post = fmaf(p.gate ? p.gate[(size_t)g * p.H + out] : 1.0f, a, post);
             }
         }
+        if (mine && p.dw_post)
+            p.dw_post[out] = post;
+        return;
     }
-    post = across(post);
-    if (w == 0 && in && p.dw_post)
-        p.dw_post[h] = post;
+    // many groups: each by one slice
+    float4 wp = make_float4(1.f, 1.f, 1.f, 1.f), post = zero;
+    if (in && p.w_post)
+        wp = *reinterpret_cast<const float4 *>(p.w_post + h);
+    if (in)
+        for (int g = slice; g < p.groups; g += 128) {
+            const float4 a = some(p.part_a, (size_t)g * p.cpg, p.cpg, 0, 1);
+            const size_t at = (size_t)g * p.H + h;
+            if (p.d_gate) {
+                p.d_gate[at] = wp.x * a.x;
+                p.d_gate[at + 1] = wp.y * a.y;
+                p.d_gate[at + 2] = wp.z * a.z;
+                p.d_gate[at + 3] = wp.w * a.w;
+            }
+            float4 q = make_float4(1.f, 1.f, 1.f, 1.f);
+            if (p.gate)
+                q = *reinterpret_cast<const float4 *>(p.gate + at);
+            post.x = fmaf(q.x, a.x, post.x);
+            post.y = fmaf(q.y, a.y, post.y);
+            post.z = fmaf(q.z, a.z, post.z);
+            post.w = fmaf(q.w, a.w, post.w);
+        }
+    const float total = across(post);
+    if (mine && p.dw_post)
+        p.dw_post[out] = total;
 }
 
 namespace {
 
-struct Shape {
+// Forward: vectors per lane, warps per row.
+struct FwdShape {
+    int vpt, w;
+};
+
+FwdShape fwd_shape(int H)
+{
+    const int nv = H / 8;
+    if (nv <= 256)
+        return {nv <= 32 ? 1 : nv <= 64 ? 2 : nv <= 128 ? 4 : 8, 1};
+    return {8, nv <= 512 ? 2 : 4};
+}
+
+// Backward: vectors per thread, threads of a row's block.
+struct BwdShape {
     int vpt, threads;
 };
 
-// Sixteen columns per thread (eight where a warp then covers the row): a
-// thread's share of the reductions costs half as much per column.
-Shape shape_of(int H)
+BwdShape bwd_shape(int H)
 {
     const int nv = H / 8;
     const int vpt = nv <= 32 ? 1 : 2;
@@ -625,14 +717,10 @@ Shape shape_of(int H)
     return {vpt, (per + 31) / 32 * 32};
 }
 
-template <int VPT, bool F32, bool HAS_Y>
-cudaError_t launch_one(const BlockNormParams &p, bool bwd, int threads, int blocks, cudaStream_t s)
+cudaError_t launch(void (*kernel)(BlockNormParams), const BlockNormParams &p, int blocks, int threads, size_t smem,
+                   cudaStream_t s)
 {
-    auto kernel = bwd ? block_norm_backward_kernel<VPT, F32, HAS_Y> : block_norm_kernel<VPT, F32, HAS_Y>;
-    using B = Ring<F32, HAS_Y, true>;
-    using A = Ring<F32, HAS_Y, false>;
-    const size_t smem = (size_t)(bwd ? B::ROWS * B::PIECES : A::ROWS * A::PIECES) * VPT * threads * 16;
-    if (smem > 40 * 1024) {      // (with the kernels' static 1.2 KB, past the 48 KB that need no opting in)
+    if (smem > 40 * 1024) {          // (with the static arrays, past the 48 KB that need no opting in)
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess)
             return e;
@@ -641,49 +729,81 @@ cudaError_t launch_one(const BlockNormParams &p, bool bwd, int threads, int bloc
     return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
 
-cudaError_t launch_any(const BlockNormParams &p, bool f32, bool bwd, int blocks, cudaStream_t s)
+template <int VPT, int W>
+cudaError_t launch_fwd(const BlockNormParams &p, bool f32, int blocks, cudaStream_t s)
 {
-    const Shape sh = shape_of(p.H);
     const bool y = p.y != nullptr;
-    if (sh.vpt == 1)
-        return f32 ? (y ? launch_one<1, true, true>(p, bwd, sh.threads, blocks, s)
-                        : launch_one<1, true, false>(p, bwd, sh.threads, blocks, s))
-                   : (y ? launch_one<1, false, true>(p, bwd, sh.threads, blocks, s)
-                        : launch_one<1, false, false>(p, bwd, sh.threads, blocks, s));
-    return f32 ? (y ? launch_one<2, true, true>(p, bwd, sh.threads, blocks, s)
-                    : launch_one<2, true, false>(p, bwd, sh.threads, blocks, s))
-               : (y ? launch_one<2, false, true>(p, bwd, sh.threads, blocks, s)
-                    : launch_one<2, false, false>(p, bwd, sh.threads, blocks, s));
+    const int pieces = (f32 ? 2 : 1) + (y ? 1 : 0);
+    // the rows' slots, then the weights' copies (160 KB at most)
+    const size_t smem = (size_t)VPT * pieces * BN_THREADS * 16 + 8ull * p.H;
+    return launch(f32 ? (y ? block_norm_kernel<VPT, W, true, true> : block_norm_kernel<VPT, W, true, false>)
+                      : (y ? block_norm_kernel<VPT, W, false, true> : block_norm_kernel<VPT, W, false, false>),
+                  p, blocks, BN_THREADS, smem, s);
+}
+
+template <int VPT>
+cudaError_t launch_bwd(const BlockNormParams &p, bool f32, int blocks, int threads, cudaStream_t s)
+{
+    const bool y = p.y != nullptr;
+    const int pieces = (f32 ? 4 : 2) + (y ? 2 : 1);
+    const size_t smem = (size_t)(f32 ? Slots<true, true, true>::ROWS : Slots<false, true, true>::ROWS) * VPT * pieces *
+                        threads * 16;
+    return launch(f32 ? (y ? block_norm_backward_kernel<VPT, true, true> : block_norm_backward_kernel<VPT, true, false>)
+                      : (y ? block_norm_backward_kernel<VPT, false, true>
+                           : block_norm_backward_kernel<VPT, false, false>),
+                  p, blocks, threads, smem, s);
 }
 
 }  // namespace
 
-// Blocks that a launch fills the GPU with: 512 threads per SM (at the 128
-// registers that the launch bounds allow, what the register file holds), so
-// that a block's rows are contiguous and its weights are loaded once.
+// Forward: rows go round the blocks first, so that a few rows spread over the
+// SMs.  Narrow rows leave room for several blocks per SM.
 int block_norm_blocks(int T, int H, int sms)
 {
-    const Shape sh = shape_of(H);
-    const int per_sm = 512 / sh.threads;
-    const int n = sms * (per_sm < 1 ? 1 : per_sm);
+    const int vpt = fwd_shape(H).vpt;
+    const int n = sms * (vpt >= 8 ? 2 : vpt >= 4 ? 3 : 6);
     return T < n ? T : n;
 }
 
-int block_norm_cpg(int T, int groups, int blocks)
+// Backward: 512 threads per SM (at the 128 registers that the launch bounds
+// allow, what the register file holds).  The chunks per gate group are those
+// with the fewest rows in the longest-working block, and of equal ones the most.
+BlockNormPlan block_norm_plan(int T, int H, int groups, int sms)
 {
     const int rows = T / groups;
-    int cpg = (blocks + groups - 1) / groups;
-    return cpg < 1 ? 1 : cpg > rows ? rows : cpg;
+    const int most = sms * (512 / bwd_shape(H).threads);
+    BlockNormPlan best = {};
+    long long least = -1;
+    for (int m = 0; m <= 4; ++m) {       // one chunk per group, or as many as fill the blocks m times
+        const long long want = m ? (long long)m * most / groups : 1;
+        const int cpg = (int)(want < 1 ? 1 : want > rows ? rows : want);
+        const long long chunks = (long long)groups * cpg;
+        const long long cost = (chunks + most - 1) / most * ((rows + cpg - 1) / cpg);
+        if (least < 0 || cost < least || (cost == least && chunks <= most)) {
+            least = cost;
+            best.cpg = cpg;
+            best.blocks = (int)(chunks < most ? chunks : most);
+        }
+    }
+    return best;
 }
 
 cudaError_t launch_block_norm(const BlockNormParams &p, bool stream_f32, int blocks, cudaStream_t s)
 {
-    return launch_any(p, stream_f32, false, blocks, s);
+    const FwdShape sh = fwd_shape(p.H);
+    if (sh.w == 1)
+        return sh.vpt == 1   ? launch_fwd<1, 1>(p, stream_f32, blocks, s)
+               : sh.vpt == 2 ? launch_fwd<2, 1>(p, stream_f32, blocks, s)
+               : sh.vpt == 4 ? launch_fwd<4, 1>(p, stream_f32, blocks, s)
+                             : launch_fwd<8, 1>(p, stream_f32, blocks, s);
+    return sh.w == 2 ? launch_fwd<8, 2>(p, stream_f32, blocks, s) : launch_fwd<8, 4>(p, stream_f32, blocks, s);
 }
 
 cudaError_t launch_block_norm_backward(const BlockNormParams &p, bool stream_f32, int blocks, cudaStream_t s)
 {
-    return launch_any(p, stream_f32, true, blocks, s);
+    const BwdShape sh = bwd_shape(p.H);
+    return sh.vpt == 1 ? launch_bwd<1>(p, stream_f32, blocks, sh.threads, s)
+                       : launch_bwd<2>(p, stream_f32, blocks, sh.threads, s);
 }
 
 cudaError_t launch_block_norm_finish(const BlockNormParams &p, int blocks, cudaStream_t s)

@@ -431,7 +431,10 @@ struct BlockNormParams {
 };
 constexpr int BLOCK_NORM_MAX_H = 8192;   // a row is one block's registers
 int block_norm_blocks(int T, int H, int sms);
-int block_norm_cpg(int T, int groups, int blocks);
+struct BlockNormPlan {
+    int blocks, cpg;
+};
+BlockNormPlan block_norm_plan(int T, int H, int groups, int sms);
 cudaError_t launch_block_norm(const BlockNormParams &p, bool stream_f32, int blocks, cudaStream_t s);
 cudaError_t launch_block_norm_backward(const BlockNormParams &p, bool stream_f32, int blocks, cudaStream_t s);
 cudaError_t launch_block_norm_finish(const BlockNormParams &p, int blocks, cudaStream_t s);
