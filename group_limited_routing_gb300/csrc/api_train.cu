@@ -139,10 +139,10 @@ int vocab_group(int H) { return std::max(1, (32 << 20) / (256 * 2 * H)); }
 
 // The logits product's operands: rows of hidden (packed or not), rows of W.
 bool vocab_logits_maps(PairGemmParams &p, const VocabLayout &L, int T, int H, int V, const moe_bf16 *hidden,
-                       const moe_bf16 *W, void *ws)
+                       const moe_bf16 *W, void *ws, int a_rows)
 {
-    return make_map_bf16(&p.tmA, hidden, T, H, GEMM_BK, 128) &&
-           make_map_bf16(&p.tmHidden, at<uint16_t>(ws, L.hidden), T, H, GEMM_BK, 128) &&
+    return make_map_bf16(&p.tmA, hidden, T, H, GEMM_BK, a_rows) &&
+           make_map_bf16(&p.tmHidden, at<uint16_t>(ws, L.hidden), T, H, GEMM_BK, a_rows) &&
            make_map_bf16(&p.tmB, W, V, H, GEMM_BK, 128);
 }
 
@@ -312,13 +312,16 @@ int moe_vocab_loss(int32_t T, int32_t H, int32_t V, const moe_bf16 *hidden, cons
     rp.row_of = at<int>(ws, L.row_of);
     rp.packed_target = at<int>(ws, L.target);
     rp.status = status;
+    rp.hidden = hidden;
+    rp.packed = at<uint16_t>(ws, L.hidden);
+    rp.H = H;
     rp.loss = loss;
     rp.lse_out = lse;
     GLR_LAUNCH(KID_VOCAB_ROWS, launch_vocab_rows(rp, s));
-    GLR_LAUNCH(KID_VOCAB_ROWS, launch_vocab_pack(hidden, meta, rp.row_of, T, H, at<uint16_t>(ws, L.hidden), s));
+    const bool few = T <= PAIR_FEW_ROWS;
     PairGemmParams p;
     memset(&p, 0, sizeof(p));
-    if (!vocab_logits_maps(p, L, T, H, V, hidden, W_vocab, ws))
+    if (!vocab_logits_maps(p, L, T, H, V, hidden, W_vocab, ws, few ? PAIR_FEW_ROWS : 128))
         return MOE_ERR_CUDA;
     p.T = T;
     p.meta = meta;
@@ -334,7 +337,8 @@ int moe_vocab_loss(int32_t T, int32_t H, int32_t V, const moe_bf16 *hidden, cons
     p.ld_stats = T;
     p.target_logit = at<float>(ws, L.logit);
     p.status = status;
-    GLR_LAUNCH(KID_VOCAB_LOGITS, launch_pair_gemm(PG_STATS, false, false, p, ceil_div(T, 256) * L.ntiles, s));
+    GLR_LAUNCH(KID_VOCAB_LOGITS, launch_pair_gemm(few ? PG_STATS_FEW : PG_STATS, false, false, p, ceil_div(T, 256) * L.ntiles,
+                                                   s));
     GLR_LAUNCH(KID_VOCAB_JOIN, launch_vocab_join(p.stats, L.nstats, T, p.target_logit, meta, rp.row_of, T, loss, lse,
                                                  s));
     set_last_launches(launches);
@@ -379,13 +383,15 @@ int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hid
     rp.row_of = at<int>(ws, L.row_of);
     rp.packed_target = at<int>(ws, L.target);
     rp.status = status;
+    rp.hidden = hidden;
+    rp.packed = at<uint16_t>(ws, L.hidden);
+    rp.H = H;
     rp.packed_of = at<int>(ws, L.packed_of);
     rp.lse = lse;
     rp.d_loss = d_loss;
     rp.packed_lse = at<float>(ws, L.lse);
     rp.packed_weight = at<float>(ws, L.weight);
     GLR_LAUNCH(KID_VOCAB_ROWS, launch_vocab_rows(rp, s));
-    GLR_LAUNCH(KID_VOCAB_ROWS, launch_vocab_pack(hidden, meta, rp.row_of, T, H, at<uint16_t>(ws, L.hidden), s));
 
     uint16_t *dz = at<uint16_t>(ws, L.dz);
     float *part = at<float>(ws, L.part);
@@ -393,7 +399,7 @@ int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hid
     // z again, piece by piece, turned into dz in the epilogue
     PairGemmParams pz, px, pw;
     memset(&pz, 0, sizeof(pz));
-    if (!vocab_logits_maps(pz, L, T, H, V, hidden, W_vocab, ws) ||
+    if (!vocab_logits_maps(pz, L, T, H, V, hidden, W_vocab, ws, 128) ||
         !make_map_bf16(&pz.tmOut, dz, T, L.piece, 64, 32))
         return MOE_ERR_CUDA;
     pz.T = T;

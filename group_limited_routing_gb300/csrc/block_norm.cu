@@ -22,9 +22,11 @@
 // memory of its own (cp.async), so loads in flight cost no registers and no
 // thread waits for another's copies, and the arithmetic runs on pairs of fp32
 // values (f32x2).
-//   Forward: a row belongs to one warp up to H = 2048 (two up to 4096, four
-//   above), so that 64 columns per lane share each reduction; a row's piece is
-//   fetched for the next row as soon as it has been read.
+//   Forward: a row belongs to one warp up to H = 2048, so that 64 columns per
+//   lane share each reduction and none needs a barrier; a row's piece is
+//   fetched for the next row as soon as it has been read.  Wider rows belong to
+//   a block, 16 columns per thread (several warps per row with 64 columns per
+//   lane measured WIDE_FIGURES).
 //   Backward: a row belongs to a block, 16 columns per thread, because the
 //   column sums of all its rows stay in the threads' registers; rows are
 //   fetched three (fp32 stream: two) ahead.  One warp per row with 64 columns
@@ -39,8 +41,8 @@ namespace glr {
 
 namespace {
 
-constexpr int BN_WARPS = 8;          // forward: warps of a block, 8 / W rows at a time
-constexpr int BN_BWD_WARPS = 16;     // backward: warps of a row at most
+constexpr int BN_WARPS = 8;          // forward, a warp per row: rows of a block at a time
+constexpr int BN_BWD_WARPS = 16;     // a block per row: its warps at most
 
 // two fp32 values in one register pair
 struct F2 {
@@ -146,34 +148,11 @@ struct Vec8<true> {
     }
 };
 
-// the W warps of a row meet
-template <int W>
-__device__ __forceinline__ void row_barrier(int group)
-{
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * W) : "memory");
-}
-
-// Sum over a row's warps, the same bits in every thread (a butterfly, then the
-// warps' sums in warp order).  `slot` alternates between calls, so one barrier
-// per call suffices: a slot is written again only after the barrier of the call
-// between, which every reader of it has passed.
-template <int W>
-__device__ __forceinline__ float row_sum(float v, float (*sm)[BN_WARPS], int &slot)
+__device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
         v += __shfl_xor_sync(0xffffffffu, v, off);
-    if (W == 1)
-        return v;
-    const int warp = threadIdx.x >> 5, group = warp / W;
-    if ((threadIdx.x & 31) == 0)
-        sm[slot][warp] = v;
-    row_barrier<W>(group);
-    v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < W; ++w)
-        v += sm[slot][group * W + w];
-    slot ^= 1;
     return v;
 }
 
@@ -183,9 +162,7 @@ __device__ __forceinline__ float row_sum(float v, float (*sm)[BN_WARPS], int &sl
 // the call between, which every reader of it has passed.
 __device__ __forceinline__ float block_sum(float v, float (*sm)[BN_BWD_WARPS], int &slot)
 {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-        v += __shfl_xor_sync(0xffffffffu, v, off);
+    v = warp_sum(v);
     const int nw = blockDim.x >> 5;
     if (nw == 1)
         return v;
@@ -287,7 +264,7 @@ struct Slots {
     static constexpr int X = F32 ? 2 : 1;
     static constexpr int AT_Y = X, AT_DN = X + (HAS_Y ? 1 : 0), AT_DR = AT_DN + 1;
     static constexpr int PIECES = BWD ? AT_DR + X : AT_DN;
-    static constexpr int ROWS = F32 ? 2 : 3;
+    static constexpr int ROWS = (F32 ? 2 : 3) + (BWD ? 0 : 1);
 };
 
 // The weights' copies in shared memory, behind the rows' slots.
@@ -310,25 +287,24 @@ __device__ __forceinline__ void stage_weights(const BlockNormParams &p, uint4 *a
 
 }  // namespace
 
-// Row group g of block b takes rows g grid + b, and every (groups grid)-th after.
-template <int VPT, int W, bool F32, bool HAS_Y>
+// A warp per row: warp w of block b takes rows w grid + b, and every (warps grid)-th
+// after.
+template <int VPT, bool F32, bool HAS_Y>
 __global__ void __launch_bounds__(BN_THREADS) block_norm_kernel(const BlockNormParams p)
 {
     using X = Vec8<F32>;
     using S = Slots<F32, HAS_Y, false>;
     extern __shared__ uint4 dyn[];       // [VPT][PIECES][threads], weights
-    __shared__ float sm[2][BN_WARPS];
     pdl_wait();
     const int nv = p.H / 8;
     const float inv_h = 1.0f / (float)p.H;
     const F2 alpha = f2(p.alpha);
-    const int group = threadIdx.x / (32 * W), lane = threadIdx.x % (32 * W);
-    const int step = (BN_WARPS / W) * gridDim.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int step = BN_WARPS * gridDim.x;
     uint4 *mine = dyn + threadIdx.x;
     const uint32_t mine_s = smem_u32(mine);
-    int slot = 0;
     auto fetch = [&](int k, int row) {
-        const int v = lane + k * 32 * W;
+        const int v = lane + k * 32;
         if (row < p.T && v < nv) {
             const size_t at = (size_t)row * nv + v;
             const uint32_t dst = mine_s + k * S::PIECES * BN_THREADS * 16;
@@ -339,7 +315,7 @@ __global__ void __launch_bounds__(BN_THREADS) block_norm_kernel(const BlockNormP
                 cp_async16(dst + S::AT_Y * BN_THREADS * 16, reinterpret_cast<const uint4 *>(p.y) + at);
         }
     };
-    int row = group * gridDim.x + blockIdx.x;
+    int row = warp * gridDim.x + blockIdx.x;
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
         fetch(k, row);
@@ -353,20 +329,20 @@ __global__ void __launch_bounds__(BN_THREADS) block_norm_kernel(const BlockNormP
             F2 s = f2(0.0f);
 #pragma unroll
             for (int k = 0; k < VPT; ++k)
-                if (lane + k * 32 * W < nv) {
+                if (lane + k * 32 < nv) {
                     F2 y[4];
                     unpack8(mine[(k * S::PIECES + S::AT_Y) * BN_THREADS], y);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         s = fma2(y[i], y[i], s);
                 }
-            rho = f2(rsqrtf(row_sum<W>(sum2(s), sm, slot) * inv_h + p.eps));
+            rho = f2(rsqrtf(warp_sum(sum2(s)) * inv_h + p.eps));
         }
         F2 r[VPT][4];
         F2 s = f2(0.0f);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int v = lane + k * 32 * W;
+            const int v = lane + k * 32;
             if (v < nv) {
                 const uint4 *at = mine + k * S::PIECES * BN_THREADS;
                 X::read(at, BN_THREADS, r[k]);
@@ -388,10 +364,10 @@ __global__ void __launch_bounds__(BN_THREADS) block_norm_kernel(const BlockNormP
                 fetch(k, row + step);
             }
         }
-        const F2 sigma = f2(rsqrtf(row_sum<W>(sum2(s), sm, slot) * inv_h + p.eps));
+        const F2 sigma = f2(rsqrtf(warp_sum(sum2(s)) * inv_h + p.eps));
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int v = lane + k * 32 * W;
+            const int v = lane + k * 32;
             if (v < nv) {
                 if (p.r)
                     X::store(p.r, (size_t)row * nv + v, r[k]);
@@ -404,6 +380,114 @@ __global__ void __launch_bounds__(BN_THREADS) block_norm_kernel(const BlockNormP
             }
         }
     }
+}
+
+// Rows wider than a warp's registers hold (H > 2048): a block per row, rows
+// fetched four (fp32 stream: three) ahead.  Block b takes rows [b T / grid, (b + 1) T / grid).
+template <int VPT, bool F32, bool HAS_Y>
+__global__ void __launch_bounds__(512) block_norm_wide_kernel(const BlockNormParams p)
+{
+    using X = Vec8<F32>;
+    using At = Slots<F32, HAS_Y, false>;
+    constexpr int P = At::PIECES, S = At::ROWS;
+    extern __shared__ uint4 ring[];      // [S][VPT][P][threads]
+    __shared__ float sm[2][BN_BWD_WARPS];
+    pdl_wait();
+    const int nt = blockDim.x;
+    const int nv = p.H / 8;
+    const int row0 = (int)((long long)blockIdx.x * p.T / gridDim.x);
+    const int row1 = (int)((long long)(blockIdx.x + 1) * p.T / gridDim.x);
+    const float inv_h = 1.0f / (float)p.H;
+    const F2 alpha = f2(p.alpha);
+    int slot = 0, group = -1;
+    uint4 *mine = ring + threadIdx.x;
+    auto fetch = [&](int row, int st) {
+        if (row < row1)
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int v = threadIdx.x + k * nt;
+                if (v < nv) {
+                    const size_t at = (size_t)row * nv + v;
+                    const uint32_t dst = smem_u32(mine + (st * VPT + k) * P * nt);
+#pragma unroll
+                    for (int i = 0; i < X::PIECES; ++i)
+                        cp_async16(dst + i * nt * 16, static_cast<const uint4 *>(p.x) + at * X::PIECES + i);
+                    if (HAS_Y)
+                        cp_async16(dst + X::PIECES * nt * 16, reinterpret_cast<const uint4 *>(p.y) + at);
+                }
+            }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int st = 0; st < S; ++st)
+        fetch(row0 + st, st);
+    F2 gw[VPT][4], wpre[VPT][4];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int v = threadIdx.x + k * nt;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            gw[k][i] = wpre[k][i] = f2(0.0f);
+        if (v < nv)
+            load_vec(p.w_pre, v, wpre[k]);
+    }
+    int st = 0;
+    for (int row = row0; row < row1; ++row) {
+        if (HAS_Y && row / p.rows_per_gate != group) {
+            group = row / p.rows_per_gate;
+            load_gw_columns<VPT>(p, group, nv, gw);
+        }
+        cp_async_wait<S - 1>();
+        F2 r[VPT][4], y[VPT][4];
+        F2 s = f2(0.0f);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                r[k][i] = y[k][i] = f2(0.0f);
+            if (threadIdx.x + k * nt < nv) {
+                const uint4 *at = mine + (st * VPT + k) * P * nt;
+                X::read(at, nt, r[k]);
+                if (HAS_Y) {
+                    unpack8(at[X::PIECES * nt], y[k]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s = fma2(y[k][i], y[k][i], s);
+                }
+            }
+        }
+        fetch(row + S, st);
+        st = st + 1 == S ? 0 : st + 1;
+        F2 rho = f2(0.0f);
+        if (HAS_Y)
+            rho = f2(rsqrtf(block_sum(sum2(s), sm, slot) * inv_h + p.eps));
+        s = f2(0.0f);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (HAS_Y)
+                    r[k][i] = fma2(alpha, r[k][i], mul2(gw[k][i], mul2(y[k][i], rho)));
+                else
+                    r[k][i] = mul2(alpha, r[k][i]);
+                s = fma2(r[k][i], r[k][i], s);
+            }
+        const F2 sigma = f2(rsqrtf(block_sum(sum2(s), sm, slot) * inv_h + p.eps));
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = threadIdx.x + k * nt;
+            if (v >= nv)
+                continue;
+            if (p.r)
+                X::store(p.r, (size_t)row * nv + v, r[k]);
+            F2 n[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                n[i] = mul2(mul2(r[k][i], sigma), wpre[k][i]);
+            Vec8<false>::store(p.n, (size_t)row * nv + v, n);
+        }
+    }
+    cp_async_wait<0>();
 }
 
 // Chunk c holds rows of one gate group only: group c / cpg, its part c % cpg of
@@ -691,25 +775,21 @@ __global__ void __launch_bounds__(1024) block_norm_finish_kernel(const BlockNorm
 
 namespace {
 
-// Forward: vectors per lane, warps per row.
-struct FwdShape {
-    int vpt, w;
-};
-
-FwdShape fwd_shape(int H)
+// Forward, a warp per row: vectors per lane.
+int lane_vectors(int H)
 {
     const int nv = H / 8;
-    if (nv <= 256)
-        return {nv <= 32 ? 1 : nv <= 64 ? 2 : nv <= 128 ? 4 : 8, 1};
-    return {8, nv <= 512 ? 2 : 4};
+    return nv <= 32 ? 1 : nv <= 64 ? 2 : nv <= 128 ? 4 : 8;
 }
 
-// Backward: vectors per thread, threads of a row's block.
-struct BwdShape {
+constexpr int BN_WARP_MAX_H = 2048;
+
+// A block per row: vectors per thread, threads.
+struct RowShape {
     int vpt, threads;
 };
 
-BwdShape bwd_shape(int H)
+RowShape row_shape(int H)
 {
     const int nv = H / 8;
     const int vpt = nv <= 32 ? 1 : 2;
@@ -729,16 +809,27 @@ cudaError_t launch(void (*kernel)(BlockNormParams), const BlockNormParams &p, in
     return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
 
-template <int VPT, int W>
+template <int VPT>
 cudaError_t launch_fwd(const BlockNormParams &p, bool f32, int blocks, cudaStream_t s)
 {
     const bool y = p.y != nullptr;
     const int pieces = (f32 ? 2 : 1) + (y ? 1 : 0);
-    // the rows' slots, then the weights' copies (160 KB at most)
+    // the rows' slots, then the weights' copies (112 KB at most)
     const size_t smem = (size_t)VPT * pieces * BN_THREADS * 16 + 8ull * p.H;
-    return launch(f32 ? (y ? block_norm_kernel<VPT, W, true, true> : block_norm_kernel<VPT, W, true, false>)
-                      : (y ? block_norm_kernel<VPT, W, false, true> : block_norm_kernel<VPT, W, false, false>),
+    return launch(f32 ? (y ? block_norm_kernel<VPT, true, true> : block_norm_kernel<VPT, true, false>)
+                      : (y ? block_norm_kernel<VPT, false, true> : block_norm_kernel<VPT, false, false>),
                   p, blocks, BN_THREADS, smem, s);
+}
+
+cudaError_t launch_wide(const BlockNormParams &p, bool f32, int blocks, int threads, cudaStream_t s)
+{
+    const bool y = p.y != nullptr;
+    const int pieces = (f32 ? 2 : 1) + (y ? 1 : 0);
+    const size_t smem = (size_t)(f32 ? Slots<true, true, false>::ROWS : Slots<false, true, false>::ROWS) * 2 * pieces *
+                        threads * 16;
+    return launch(f32 ? (y ? block_norm_wide_kernel<2, true, true> : block_norm_wide_kernel<2, true, false>)
+                      : (y ? block_norm_wide_kernel<2, false, true> : block_norm_wide_kernel<2, false, false>),
+                  p, blocks, threads, smem, s);
 }
 
 template <int VPT>
@@ -757,11 +848,12 @@ cudaError_t launch_bwd(const BlockNormParams &p, bool f32, int blocks, int threa
 }  // namespace
 
 // Forward: rows go round the blocks first, so that a few rows spread over the
-// SMs.  Narrow rows leave room for several blocks per SM.
+// SMs; narrow rows leave room for several blocks per SM.  A block per row: 512
+// threads per SM, as backward.
 int block_norm_blocks(int T, int H, int sms)
 {
-    const int vpt = fwd_shape(H).vpt;
-    const int n = sms * (vpt >= 8 ? 2 : vpt >= 4 ? 3 : 6);
+    const int vpt = lane_vectors(H);
+    const int n = sms * (H > BN_WARP_MAX_H ? 512 / row_shape(H).threads : vpt >= 8 ? 2 : vpt >= 4 ? 3 : 6);
     return T < n ? T : n;
 }
 
@@ -771,7 +863,7 @@ int block_norm_blocks(int T, int H, int sms)
 BlockNormPlan block_norm_plan(int T, int H, int groups, int sms)
 {
     const int rows = T / groups;
-    const int most = sms * (512 / bwd_shape(H).threads);
+    const int most = sms * (512 / row_shape(H).threads);
     BlockNormPlan best = {};
     long long least = -1;
     for (int m = 0; m <= 4; ++m) {       // one chunk per group, or as many as fill the blocks m times
@@ -790,18 +882,19 @@ BlockNormPlan block_norm_plan(int T, int H, int groups, int sms)
 
 cudaError_t launch_block_norm(const BlockNormParams &p, bool stream_f32, int blocks, cudaStream_t s)
 {
-    const FwdShape sh = fwd_shape(p.H);
-    if (sh.w == 1)
-        return sh.vpt == 1   ? launch_fwd<1, 1>(p, stream_f32, blocks, s)
-               : sh.vpt == 2 ? launch_fwd<2, 1>(p, stream_f32, blocks, s)
-               : sh.vpt == 4 ? launch_fwd<4, 1>(p, stream_f32, blocks, s)
-                             : launch_fwd<8, 1>(p, stream_f32, blocks, s);
-    return sh.w == 2 ? launch_fwd<8, 2>(p, stream_f32, blocks, s) : launch_fwd<8, 4>(p, stream_f32, blocks, s);
+    if (p.H > BN_WARP_MAX_H)
+        return launch_wide(p, stream_f32, blocks, row_shape(p.H).threads, s);
+    switch (lane_vectors(p.H)) {
+    case 1: return launch_fwd<1>(p, stream_f32, blocks, s);
+    case 2: return launch_fwd<2>(p, stream_f32, blocks, s);
+    case 4: return launch_fwd<4>(p, stream_f32, blocks, s);
+    default: return launch_fwd<8>(p, stream_f32, blocks, s);
+    }
 }
 
 cudaError_t launch_block_norm_backward(const BlockNormParams &p, bool stream_f32, int blocks, cudaStream_t s)
 {
-    const BwdShape sh = bwd_shape(p.H);
+    const RowShape sh = row_shape(p.H);
     return sh.vpt == 1 ? launch_bwd<1>(p, stream_f32, blocks, sh.threads, s)
                        : launch_bwd<2>(p, stream_f32, blocks, sh.threads, s);
 }

@@ -68,7 +68,8 @@ __device__ __forceinline__ float rcp_approx(float x)
 // -87 so that 1 + e stays finite (the clamp moves s by less than 2e-38).  Not
 // correctly rounded: the test suite measures its distance from an exact
 // sigmoid.
-__device__ __forceinline__ float router_sigmoid(float L)
+// (`e`: the exp(-L) it was formed from.)
+__device__ __forceinline__ float router_sigmoid(float L, float &e)
 {
     constexpr float LOG2E_HI = 1.44269502162933349609375f;   // log2(e) rounded to fp32
     constexpr float LOG2E_LO = 1.925963033500011e-08f;       // log2(e) - LOG2E_HI
@@ -77,11 +78,17 @@ __device__ __forceinline__ float router_sigmoid(float L)
     const float a = -x * LOG2E_HI;
     float r = fmaf(-x, LOG2E_HI, -a);                         // (-x) LOG2E_HI - a, exactly
     r = fmaf(-x, LOG2E_LO, r);
-    float e = ex2_approx(a);
+    e = ex2_approx(a);
     e = fmaf(e, r * LN2, e);
     const float d = 1.0f + e;
     const float y = rcp_approx(d);
     return fmaf(y, fmaf(-d, y, 1.0f), y);
+}
+
+__device__ __forceinline__ float router_sigmoid(float L)
+{
+    float e;
+    return router_sigmoid(L, e);
 }
 
 // Order-preserving map of fp32 onto uint32 (for non-NaN values): a > b as
@@ -338,7 +345,9 @@ cudaError_t launch_expert_feedback(const int32_t *counts, int E, int T, int k, f
 //   PG_PARTIAL  fp32, stored or added to what is there (one slice per K split)
 //   PG_BF16     bf16( scale z )
 //   PG_BF16_ADD bf16( z + add )
-enum PairEpilogue { PG_STATS = 0, PG_DLOGITS = 1, PG_PARTIAL = 2, PG_BF16 = 3, PG_BF16_ADD = 4 };
+//   PG_STATS_FEW PG_STATS for M <= PAIR_FEW_ROWS (the A map's boxes are that many rows)
+enum PairEpilogue { PG_STATS = 0, PG_DLOGITS = 1, PG_PARTIAL = 2, PG_BF16 = 3, PG_BF16_ADD = 4, PG_STATS_FEW = 5 };
+constexpr int PAIR_FEW_ROWS = 32;
 
 // What the vocabulary operators' row kernel leaves for the kernels after it.
 struct VocabMeta {
@@ -386,6 +395,9 @@ struct VocabRowsParams {
     int *row_of;              // packed row -> row
     int *packed_target;
     int *status;
+    const uint16_t *hidden;   // [T, H]
+    uint16_t *packed;         // the counting rows' copies where some row does not count
+    int H;
     float *loss, *lse_out;    // forward: zeroed where a row does not count
     // backward
     int *packed_of;           // row -> packed row, or -1
@@ -393,8 +405,6 @@ struct VocabRowsParams {
     float *packed_lse, *packed_weight;
 };
 cudaError_t launch_vocab_rows(const VocabRowsParams &p, cudaStream_t s);
-cudaError_t launch_vocab_pack(const uint16_t *hidden, const VocabMeta *meta, const int *row_of, int T, int H,
-                              uint16_t *packed, cudaStream_t s);
 cudaError_t launch_vocab_join(const float2 *stats, int ntiles, int ld, const float *target_logit,
                               const VocabMeta *meta, const int *row_of, int T, float *loss, float *lse,
                               cudaStream_t s);

@@ -44,22 +44,33 @@ constexpr int PG_HALF = PG_BN / 2;               // an epilogue warp's columns
 constexpr float LOG2E = 1.44269504088896341f;
 
 constexpr int PG_ATOM = 64 * GEMM_BK * 2;        // 64 x 64 bf16, 8 KB
-constexpr int PG_A_BYTES = 2 * PG_ATOM;          // a CTA's 128 rows of A; as much of B
-constexpr int PG_STAGE_BYTES = 2 * PG_A_BYTES;
+constexpr int PG_B_BYTES = 2 * PG_ATOM;          // a CTA's 128 columns of B
 constexpr int PG_SLOTS = 2;                      // accumulators in TMEM
 constexpr int PG_TMEM_COLS = 512;
 
+template <int EPI>
+constexpr bool IS_STATS = EPI == PG_STATS || EPI == PG_STATS_FEW;
+
 // Shared memory: a ring of operand stages, and per epilogue warp the 4 KB
-// boxes its output leaves through (two where an addend arrives in them ahead of
-// the accumulator; none for the statistics).
+// boxes its output leaves through (the addend's two boxes besides, which arrive
+// a tile ahead; none for the statistics).
+// PG_STATS_FEW is for at most PAIR_FEW_ROWS rows, where the product streams B
+// from memory: a stage holds those rows of A only, and the shared memory this
+// frees goes to a deeper ring of B.  The MMA still reads 128 rows per CTA; the
+// rest alias the bytes behind and reach accumulator rows that nobody reads.
 template <int EPI>
 struct PgCfg {
-    static constexpr int BUFS = EPI == PG_STATS ? 0 : EPI == PG_BF16_ADD ? 2 : 1;
-    static constexpr int STAGES = 7 - BUFS;
+    static constexpr bool FEW = EPI == PG_STATS_FEW;
+    static constexpr int A_ROWS = FEW ? PAIR_FEW_ROWS : 128;
+    static constexpr int A_BYTES = A_ROWS * GEMM_BK * 2;
+    static constexpr int STAGE_BYTES = A_BYTES + PG_B_BYTES;
+    static constexpr int BUFS = IS_STATS<EPI> ? 0 : EPI == PG_BF16_ADD ? 3 : 1;
+    static constexpr int STAGES = FEW ? 11 : 7 - BUFS;
     static constexpr int STAGING = BUFS * PG_EPI_WARPS * 4096;
     static constexpr int NBARS = 2 * STAGES + 2 * PG_SLOTS + 1 + PG_EPI_WARPS;
-    static constexpr int SMEM = STAGES * PG_STAGE_BYTES + STAGING + 1024 /*align*/ + NBARS * 8 + 16;
+    static constexpr int SMEM = STAGES * STAGE_BYTES + STAGING + 1024 /*align*/ + NBARS * 8 + 16;
     static_assert(SMEM <= 232448, "more than 227 KB of shared memory");
+    static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms need 1024-B alignment");
 };
 
 // fp32 box added to global memory from shared memory (bulk-group completion)
@@ -306,7 +317,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
     extern __shared__ uint8_t dsmem[];
     const uint32_t raw = smem_u32(dsmem);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    uint8_t *staging = dsmem + (base - raw) + C::STAGES * PG_STAGE_BYTES;
+    uint8_t *staging = dsmem + (base - raw) + C::STAGES * C::STAGE_BYTES;
     uint64_t *bars = reinterpret_cast<uint64_t *>(staging + C::STAGING);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + C::NBARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
@@ -360,7 +371,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
     if (warp == 0) {
         if (lane == 0) {
             // ---------------------------------------------------- TMA producer
-            const CUtensorMap *ma = (packed && (EPI == PG_STATS || EPI == PG_DLOGITS)) ? &p.tmHidden : &p.tmA;
+            const CUtensorMap *ma = (packed && (IS_STATS<EPI> || EPI == PG_DLOGITS)) ? &p.tmHidden : &p.tmA;
             const CUtensorMap *mb = (packed && EPI == PG_BF16) ? &p.tmHidden : &p.tmB;
             const uint32_t full_leader0 = mapa_shared(full_bar(0), 0);
             int stage = 0;
@@ -377,16 +388,17 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
                                 ok = false;
                                 break;
                             }
-                            const uint32_t sA = base + stage * PG_STAGE_BYTES, sB = sA + PG_A_BYTES;
+                            const uint32_t sA = base + stage * C::STAGE_BYTES, sB = sA + C::A_BYTES;
                             if (leader)
-                                mbar_arrive_expect_tx(full_bar(stage), 2 * PG_STAGE_BYTES);
+                                mbar_arrive_expect_tx(full_bar(stage), C::FEW ? C::A_BYTES + 2 * PG_B_BYTES
+                                                                              : 2 * C::STAGE_BYTES);
                             const uint32_t fb = full_leader0 + 8u * stage;
                             const int k = kb * GEMM_BK;
                             if (A_MN) {
 #pragma unroll
                                 for (int q = 0; q < 2; ++q)
                                     tma_load_2d_pair(sA + q * PG_ATOM, ma, fb, m + q * 64, k + p.a_off[seg]);
-                            } else {
+                            } else if (!C::FEW || leader) {
                                 tma_load_2d_pair(sA, ma, fb, k, m + p.a_off[seg]);
                             }
                             if (B_MN) {
@@ -441,7 +453,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t sA = base + stage * PG_STAGE_BYTES, sB = sA + PG_A_BYTES;
+                        const uint32_t sA = base + stage * C::STAGE_BYTES, sB = sA + C::A_BYTES;
 #pragma unroll
                         for (int kk = 0; kk < GEMM_BK / 16; ++kk)
                             // 16 K: 32 B along a K-major row, 2048 B (two 8-row atoms) of an MN-major operand
@@ -511,10 +523,23 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
                 mbar_arrive(tempty0 + 8u * (ctr % PG_SLOTS));
             ++ctr;
         };
+        // the addend's two boxes of unit u
+        auto fetch_add = [&](int u) {
+            if (lane == 0 && u < sh.units) {
+                const Unit t = unit_of(p, sh, u);
+                const int col = t.n0 + half * PG_HALF, row = t.m0 + rank * 128 + quad * 32;
+                mbar_arrive_expect_tx(add_bar, 2 * 4096);
+                tma_load_2d(smem_u32(boxes), &p.tmHidden, add_bar, col, row);
+                tma_load_2d(smem_u32(boxes + 4096), &p.tmHidden, add_bar, col + 64, row);
+                add_pending = true;
+            }
+        };
+        if (EPI == PG_BF16_ADD)
+            fetch_add(pair);
         for (int u = pair; ok && u < sh.units; u += npairs) {
             const Unit t = unit_of(p, sh, u);
             const int row0 = t.m0 + rank * 128 + quad * 32, col0 = t.n0 + half * PG_HALF;
-            if constexpr (EPI == PG_STATS || EPI == PG_PARTIAL) {
+            if constexpr (IS_STATS<EPI> || EPI == PG_PARTIAL) {
                 uint32_t z[PG_HALF];
                 if (t.parts == 0) {
 #pragma unroll
@@ -544,23 +569,14 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
                 }
                 if (!ok)
                     break;
-                if constexpr (EPI == PG_STATS)
-                    epilogue_stats(p, sh, t, z, half, row0 + lane);
-                else
+                if constexpr (IS_STATS<EPI>) {
+                    if (row0 < sh.M)
+                        epilogue_stats(p, sh, t, z, half, row0 + lane);
+                } else
                     epilogue_partial(p, t, z, half, row0, lane, boxes);
             } else {
                 // (one part: the accumulator's values are used as they are)
                 const bool empty = t.parts == 0;
-                if constexpr (EPI == PG_BF16_ADD) {
-                    // the addend's two boxes, ahead of the accumulator
-                    if (lane == 0) {
-                        bulk_wait_group_read<0>();
-                        mbar_arrive_expect_tx(add_bar, 2 * 4096);
-                        tma_load_2d(smem_u32(boxes), &p.tmHidden, add_bar, col0, row0);
-                        tma_load_2d(smem_u32(boxes + 4096), &p.tmHidden, add_bar, col0 + 64, row0);
-                        add_pending = true;
-                    }
-                }
                 if (!empty && !accumulator()) {
                     ok = false;
                     break;
@@ -583,11 +599,11 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
                     bf16_box<true>(tacc() + 64, empty, 1.0f, boxes + 4096, lane, v[1]);
                     if (!empty)
                         release();
+                    __syncwarp();
+                    fetch_add(u + npairs);       // (every lane has read its rows of the boxes)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        fill_box(boxes + 4096 * i, v[i], lane);
-                        send_box<false>(p, boxes + 4096 * i, lane, col0 + 64 * i, row0 + p.out_row0);
-                    }
+                    for (int i = 0; i < 2; ++i)
+                        store_box<false>(p, boxes + 2 * 4096, v[i], lane, col0 + 64 * i, row0 + p.out_row0);
                 } else if constexpr (EPI == PG_BF16) {
                     uint4 v[2][8];
                     bf16_box<false>(tacc(), empty, scale, nullptr, lane, v[0]);
@@ -675,6 +691,8 @@ cudaError_t launch_pair_gemm(PairEpilogue epi, bool a_mn, bool b_mn, const PairG
 {
     if (epi == PG_STATS && !a_mn && !b_mn)
         return launch_one<PG_STATS, false, false>(p, max_units, s);
+    if (epi == PG_STATS_FEW && !a_mn && !b_mn)
+        return launch_one<PG_STATS_FEW, false, false>(p, max_units, s);
     if (epi == PG_DLOGITS && !a_mn && !b_mn)
         return launch_one<PG_DLOGITS, false, false>(p, max_units, s);
     if (epi == PG_PARTIAL && !a_mn && b_mn)

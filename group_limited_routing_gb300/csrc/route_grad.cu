@@ -37,12 +37,6 @@ __device__ __forceinline__ float logit_at(const float *logits, int nparts, long 
     return v;
 }
 
-__device__ __forceinline__ uint16_t bf16_bits(float v)
-{
-    const __nv_bfloat16 b = __float2bfloat16_rn(v);
-    return *reinterpret_cast<const uint16_t *>(&b);
-}
-
 }  // namespace
 
 // One warp per token; a lane holds EPL = E / 32 neighbouring experts.
@@ -55,6 +49,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const float *__restrict
                                                          float eps, uint16_t *parts, int *status)
 {
     constexpr int E = EPL * 32;
+    __shared__ __align__(16) float scatter[8][E];
     pdl_wait();
     const int lane = threadIdx.x & 31;
     const int warps = gridDim.x * (blockDim.x >> 5);
@@ -66,7 +61,10 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const float *__restrict
         f[i] = d_aux ? (float)counts[lane * EPL + i] / ((float)k * (float)T) : 0.0f;
     for (int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); t < T; t += warps) {
         const float *row = logits + (size_t)t * E;
-        float L[EPL], ds[EPL], s[EPL];
+        float L[EPL], ds[EPL], s[EPL], slope[EPL];
+        int e = -1;
+        if (lane < k)
+            e = idx[(size_t)t * k + lane];
 #pragma unroll
         for (int i = 0; i < EPL; i += 4) {
             const float4 q = *reinterpret_cast<const float4 *>(row + lane * EPL + i);
@@ -79,10 +77,8 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const float *__restrict
                 L[i] += q.x; L[i + 1] += q.y; L[i + 2] += q.z; L[i + 3] += q.w;
             }
         // lane j < k: the chosen expert j
-        int e = -1;
         float dw = 0.0f, sj = 0.0f;
         if (lane < k) {
-            e = idx[(size_t)t * k + lane];
             if (e < 0 || e >= E) {
                 atomicOr(status, ST_BAD_INDEX);
                 e = -1;
@@ -91,54 +87,70 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const float *__restrict
                 sj = router_sigmoid(logit_at(row, nparts, stride, e));
             }
         }
-        const float D = warp_sum(sj) + eps;
-        const float dot = warp_sum(dw * sj);
-        const float dsj = rsf / D * (dw - dot / D);
-        bool finite = true;
-        float Z = 0.0f, F = 0.0f;
+        float Z = 0.0f, F = 0.0f, zero = 0.0f;          // zero: 0 unless a logit is not finite
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            finite &= fabsf(L[i]) < INFINITY;
-            s[i] = router_sigmoid(L[i]);
+            float x;                                  // exp(-L)
+            s[i] = router_sigmoid(L[i], x);
+            slope[i] = s[i] * (L[i] > 0.0f ? x * s[i] : 1.0f - s[i]);
             Z += s[i];
             F = fmaf(f[i], s[i], F);
-            ds[i] = 0.0f;
+            zero = fmaf(L[i], 0.0f, zero);
         }
-        if (!__all_sync(0xffffffffu, finite) && lane == 0)
+        if (!__all_sync(0xffffffffu, zero == 0.0f) && lane == 0)
             atomicOr(status, ST_NONFINITE);
-        for (int j = 0; j < k; ++j) {
-            const int ej = __shfl_sync(0xffffffffu, e, j);
-            const float v = __shfl_sync(0xffffffffu, dsj, j);
-            const int at = ej - lane * EPL;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (ej >= 0 && at == i)
-                    ds[i] += v;
+        const float D = warp_sum(sj) + eps;
+        const float m = __fdividef(warp_sum(dw * sj), D);
+        float dsj = __fdividef(rsf, D) * (dw - m);
+        // to the lanes that hold the experts, through shared memory; an id that
+        // a token names more than once (never the router's) adds up in the
+        // first lane that names it
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        const bool first = e >= 0 && __ffs(same) - 1 == lane;
+        if (__any_sync(0xffffffffu, e >= 0 && !first)) {
+            float sum = 0.0f;
+            for (int j = 0; j < k; ++j) {
+                const float v = __shfl_sync(0xffffffffu, dsj, j);
+                if ((same >> j) & 1u)
+                    sum += v;
+            }
+            dsj = sum;
         }
+        float *mine = scatter[threadIdx.x >> 5];
+#pragma unroll
+        for (int i = 0; i < EPL; i += 4)
+            *reinterpret_cast<float4 *>(mine + lane * EPL + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+        __syncwarp();
+        if (first)
+            mine[e] = dsj;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < EPL; i += 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(mine + lane * EPL + i);
+            ds[i] = q.x; ds[i + 1] = q.y; ds[i + 2] = q.z; ds[i + 3] = q.w;
+        }
+        __syncwarp();
         if (d_aux) {
             Z = warp_sum(Z);
             F = warp_sum(F);
-            const float c = aux / Z, m = F / Z;
+            const float c = __fdividef(aux, Z), mean = __fdividef(F, Z);
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
-                ds[i] = fmaf(c, f[i] - m, ds[i]);
+                ds[i] = fmaf(c, f[i] - mean, ds[i]);
         }
-        uint16_t h[3][EPL];
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            float v = ds[i] * s[i] * (L[i] > 0.0f ? s[i] * __expf(-L[i]) : 1.0f - s[i]);
-#pragma unroll
-            for (int q = 0; q < 3; ++q) {
-                h[q][i] = bf16_bits(v);
-                v -= __uint_as_float((uint32_t)h[q][i] << 16);
-            }
-        }
+        for (int i = 0; i < EPL; ++i)
+            ds[i] *= slope[i];
 #pragma unroll
         for (int q = 0; q < 3; ++q) {
             uint32_t o[EPL / 2];
 #pragma unroll
-            for (int i = 0; i < EPL / 2; ++i)
-                o[i] = (uint32_t)h[q][2 * i] | ((uint32_t)h[q][2 * i + 1] << 16);
+            for (int i = 0; i < EPL / 2; ++i) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(ds[2 * i], ds[2 * i + 1]);
+                o[i] = *reinterpret_cast<const uint32_t *>(&b);
+                ds[2 * i] -= __uint_as_float(o[i] << 16);
+                ds[2 * i + 1] -= __uint_as_float(o[i] & 0xffff0000u);
+            }
             uint16_t *dst = parts + ((size_t)q * T + t) * E + lane * EPL;
             if constexpr (EPL == 8)
                 *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);

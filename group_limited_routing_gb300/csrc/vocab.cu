@@ -27,30 +27,37 @@ constexpr int ROWS_THREADS = 1024;
 
 }  // namespace
 
-// One block: thread i counts the rows of its run of rows, a scan over the
-// threads gives each its first packed row.
+// Which rows count, and their packed order: thread i counts the rows of its
+// run of rows, a scan over the threads gives each its first packed row.  Every
+// block does this for all rows (a few loads per thread, and no block waits for
+// another); block 0 writes the results, and all of them, where some row does
+// not count, copy the counting rows' hidden states side by side and then zero
+// rows up to a multiple of 64 (a K block of the weight gradient).  Where every
+// row counts the products read `hidden` itself.
 __global__ void __launch_bounds__(ROWS_THREADS) vocab_rows_kernel(const VocabRowsParams p)
 {
     __shared__ int warp_sum[32];
     __shared__ float warp_max[32];
     pdl_wait();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const bool writer = blockIdx.x == 0;
     const int per = (p.T + ROWS_THREADS - 1) / ROWS_THREADS;
     const int t0 = min(p.T, (int)threadIdx.x * per), t1 = min(p.T, t0 + per);
     int n = 0;
     bool bad = false;
     float top = 0.0f;
+#pragma unroll 4
     for (int t = t0; t < t1; ++t) {
         const long long v = target_at(p, t);
         const bool counts = v != p.ignore && v >= 0 && v < p.V;
         bad |= !counts && v != p.ignore;
         n += counts;
-        if (p.d_loss && counts) {
+        if (p.d_loss && writer && counts) {
             const float g = fabsf(p.d_loss[t]);
             top = g > top || g != g ? g : top;      // a NaN stays
         }
     }
-    if (bad)
+    if (bad && writer)
         atomicOr(p.status, ST_BAD_TARGET);
     int at = n;
 #pragma unroll
@@ -74,85 +81,108 @@ __global__ void __launch_bounds__(ROWS_THREADS) vocab_rows_kernel(const VocabRow
         total += warp_sum[i];
         top = warp_max[i] > top || warp_max[i] != warp_max[i] ? warp_max[i] : top;
     }
-    const float scale = top > 0.0f && top < INFINITY ? top : 1.0f;
-    if (threadIdx.x == 0) {
-        p.meta->rows = total;
-        p.meta->scale = scale;
-    }
     int r = before + at - n;
-    for (int t = t0; t < t1; ++t) {
-        const long long v = target_at(p, t);
-        const bool counts = v != p.ignore && v >= 0 && v < p.V;
-        if (p.packed_of)
-            p.packed_of[t] = counts ? r : -1;
-        if (counts) {
-            p.row_of[r] = t;
-            p.packed_target[r] = (int)v;
-            if (p.d_loss) {
-                p.packed_lse[r] = p.lse[t];
-                p.packed_weight[r] = p.d_loss[t] / scale;
+    if (writer) {
+        const float scale = top > 0.0f && top < INFINITY ? top : 1.0f;
+        if (threadIdx.x == 0) {
+            p.meta->rows = total;
+            p.meta->scale = scale;
+        }
+        int q = r;
+#pragma unroll 4
+        for (int t = t0; t < t1; ++t) {
+            const long long v = target_at(p, t);
+            const bool counts = v != p.ignore && v >= 0 && v < p.V;
+            if (p.packed_of)
+                p.packed_of[t] = counts ? q : -1;
+            if (counts) {
+                p.row_of[q] = t;
+                p.packed_target[q] = (int)v;
+                if (p.d_loss) {
+                    p.packed_lse[q] = p.lse[t];
+                    p.packed_weight[q] = p.d_loss[t] / scale;
+                }
+                ++q;
+            } else if (p.loss) {
+                p.loss[t] = 0.0f;
+                p.lse_out[t] = 0.0f;
             }
-            ++r;
-        } else if (p.loss) {
-            p.loss[t] = 0.0f;
-            p.lse_out[t] = 0.0f;
         }
     }
-}
-
-// The counting rows' hidden states side by side, then zero rows up to a
-// multiple of 64 (a K block of the weight gradient).  Nothing to do when every
-// row counts: the products then read `hidden` itself.
-__global__ void __launch_bounds__(128) vocab_pack_kernel(const uint16_t *__restrict__ hidden, const VocabMeta *meta,
-                                                         const int *row_of, int T, int H, uint16_t *packed)
-{
-    pdl_wait();
-    const int rows = meta->rows;
-    if (rows == T)
+    if (total == p.T)
         return;
-    const int padded = min(T, (rows + 63) / 64 * 64);
-    const int nv = H / 8;
-    for (int r = blockIdx.x; r < padded; r += gridDim.x) {
-        const uint4 *src = r < rows ? reinterpret_cast<const uint4 *>(hidden) + (size_t)row_of[r] * nv : nullptr;
-        uint4 *dst = reinterpret_cast<uint4 *>(packed) + (size_t)r * nv;
-        for (int v = threadIdx.x; v < nv; v += blockDim.x)
-            dst[v] = src ? src[v] : make_uint4(0, 0, 0, 0);
+    // Block b copies the packed rows congruent to b: each thread meets its own
+    // run's rows again, a warp copies one row at a time.
+    const int nv = p.H / 8, blocks = gridDim.x;
+    const uint4 *src = reinterpret_cast<const uint4 *>(p.hidden);
+    uint4 *dst = reinterpret_cast<uint4 *>(p.packed);
+    for (int i = 0; i < per; ++i) {
+        const int t = t0 + i;
+        bool mine = false;
+        int q = 0;
+        if (t < t1) {
+            const long long v = target_at(p, t);
+            if (v != p.ignore && v >= 0 && v < p.V) {
+                q = r++;
+                mine = q % blocks == (int)blockIdx.x;
+            }
+        }
+        for (unsigned todo = __ballot_sync(0xffffffffu, mine); todo; todo &= todo - 1) {
+            const int l = __ffs(todo) - 1;
+            const size_t from = (size_t)__shfl_sync(0xffffffffu, t, l) * nv;
+            const size_t to = (size_t)__shfl_sync(0xffffffffu, q, l) * nv;
+#pragma unroll 8
+            for (int v = lane; v < nv; v += 32)
+                dst[to + v] = src[from + v];
+        }
     }
+    for (int q = total + blockIdx.x; q < min(p.T, (total + 63) / 64 * 64); q += blocks)
+        for (int v = threadIdx.x; v < nv; v += ROWS_THREADS)
+            dst[(size_t)q * nv + v] = make_uint4(0, 0, 0, 0);
 }
 
-// Joins the tiles' softmax statistics of each row: lane = row, 32 warps share
-// the tiles.  The bases are log2 values, so the sums are over powers of two.
-__global__ void __launch_bounds__(1024) vocab_join_kernel(const float2 *__restrict__ stats, int ntiles, int ld,
+// Joins the 128-column blocks' softmax statistics of each row.  A block takes R
+// rows and shares their column blocks among its 1024 / R threads per row, so
+// that a few rows' many statistics are loaded at once too.  The bases are
+// log2 values, so the sums are over powers of two; pairs are joined in a fixed
+// order (a thread's own in column order, then threads by halves).
+template <int R>
+__global__ void __launch_bounds__(1024) vocab_join_kernel(const float2 *__restrict__ stats, int nstats, int ld,
                                                           const float *__restrict__ target_logit,
                                                           const VocabMeta *meta, const int *row_of, float *loss,
                                                           float *lse)
 {
-    __shared__ float2 sm[32][33];
+    constexpr int SHARE = 1024 / R;
+    __shared__ float2 sm[1024];
     pdl_wait();
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int row = blockIdx.x * 32 + lane;
+    const int r = threadIdx.x % R, part = threadIdx.x / R;
+    const int row = blockIdx.x * R + r;
     const bool in = row < meta->rows;
-    float b = -INFINITY, s = 0.0f;
-    auto join = [&](float b2, float s2) {
-        const float top = fmaxf(b, b2);
-        if (top > -INFINITY) {
-            s = s * exp2f(b - top) + s2 * exp2f(b2 - top);
-            b = top;
-        }
+    auto join = [](float2 a, float2 b) {
+        const float top = fmaxf(a.x, b.x);
+        if (!(top > -INFINITY))
+            return a;
+        return make_float2(top, a.y * exp2f(a.x - top) + b.y * exp2f(b.x - top));
     };
-#pragma unroll 4
-    for (int i = w; i < ntiles; i += 32)
-        if (in) {
-            const float2 v = stats[(size_t)i * ld + row];
-            join(v.x, v.y);
+    float2 acc = make_float2(-INFINITY, 0.0f);
+    if (in)
+        for (int i = part; i < nstats; i += 4 * SHARE) {
+            float2 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = i + j * SHARE < nstats ? stats[(size_t)(i + j * SHARE) * ld + row]
+                                              : make_float2(-INFINITY, 0.0f);
+            acc = join(acc, join(join(v[0], v[1]), join(v[2], v[3])));
         }
-    sm[w][lane] = make_float2(b, s);
-    __syncthreads();
-    if (w != 0 || !in)
+    sm[threadIdx.x] = acc;
+    for (int half = SHARE / 2; half > 0; half >>= 1) {
+        __syncthreads();
+        if (part < half)
+            sm[threadIdx.x] = acc = join(acc, sm[threadIdx.x + half * R]);
+    }
+    if (part != 0 || !in)
         return;
-    for (int i = 1; i < 32; ++i)
-        join(sm[i][lane].x, sm[i][lane].y);
-    const float l = (b + log2f(s)) * 0.69314718055994531f;
+    const float l = (acc.x + log2f(acc.y)) * 0.69314718055994531f;
     const int t = row_of[row];
     lse[t] = l;
     loss[t] = l - target_logit[row];
@@ -191,25 +221,23 @@ __global__ void __launch_bounds__(128) vocab_dx_join_kernel(const float *__restr
 
 cudaError_t launch_vocab_rows(const VocabRowsParams &p, cudaStream_t s)
 {
-    const cudaError_t e = launch_pdl(vocab_rows_kernel, dim3(1), dim3(ROWS_THREADS), 0, s, p);
+    // an SM per block at most, and a block per eight rows: copying is spread,
+    // counting is not worth more blocks
+    const int want = (p.T + 7) / 8;
+    const cudaError_t e = launch_pdl(vocab_rows_kernel, dim3(want < 152 ? want : 152), dim3(ROWS_THREADS), 0, s, p);
     return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
 
-cudaError_t launch_vocab_pack(const uint16_t *hidden, const VocabMeta *meta, const int *row_of, int T, int H,
-                              uint16_t *packed, cudaStream_t s)
-{
-    const int blocks = T < 2432 ? T : 2432;      // 152 SMs x 16
-    const cudaError_t e = launch_pdl(vocab_pack_kernel, dim3(blocks), dim3(128), 0, s, hidden, meta, row_of, T, H,
-                                     packed);
-    return e != cudaSuccess ? e : cudaPeekAtLastError();
-}
-
-cudaError_t launch_vocab_join(const float2 *stats, int ntiles, int ld, const float *target_logit,
+cudaError_t launch_vocab_join(const float2 *stats, int nstats, int ld, const float *target_logit,
                               const VocabMeta *meta, const int *row_of, int T, float *loss, float *lse,
                               cudaStream_t s)
 {
-    const cudaError_t e = launch_pdl(vocab_join_kernel, dim3((T + 31) / 32), dim3(1024), 0, s, stats, ntiles, ld,
-                                     target_logit, meta, row_of, loss, lse);
+    // 32 rows per block read whole lines; fewer rows than fill the SMs so are
+    // spread, four to a block
+    const cudaError_t e = T > 4096 ? launch_pdl(vocab_join_kernel<32>, dim3((T + 31) / 32), dim3(1024), 0, s, stats,
+                                                nstats, ld, target_logit, meta, row_of, loss, lse)
+                                   : launch_pdl(vocab_join_kernel<4>, dim3((T + 3) / 4), dim3(1024), 0, s, stats,
+                                                nstats, ld, target_logit, meta, row_of, loss, lse);
     return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
 
