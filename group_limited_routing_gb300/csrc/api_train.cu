@@ -77,7 +77,7 @@ int choose_splits(int tiles, int kblocks, double elements, int max_splits, int m
 // K blocks per accumulator of the loss's logits (512 of K): the tensor core's
 // own running sum then stays as close to the exact one as an fp32 library
 // product's (measured, 2-norm over a batch's losses at H = 2048: PLACEHOLDER)
-constexpr int LOGIT_PART_BLOCKS = 8;
+constexpr int LOGIT_PART_BLOCKS = 11;
 
 // ---------------------------------------------------------- vocabulary loss
 int check_vocab(int32_t T, int32_t H, int32_t V, int32_t target_bits)
@@ -153,7 +153,7 @@ struct RouteBwdLayout {
 };
 
 // 64-token blocks per accumulator of the weight gradient (its K is the tokens)
-constexpr int ROUTE_DW_BLOCKS = 8;
+constexpr int ROUTE_DW_BLOCKS = 4;
 
 RouteBwdLayout route_bwd_layout(const moe_cfg &c)
 {
@@ -327,9 +327,8 @@ int moe_vocab_loss(int32_t T, int32_t H, int32_t V, const moe_bf16 *hidden, cons
     p.meta = meta;
     p.m_from_rows = 1;
     p.N = V;
-    p.nseg = 1;
     p.kblocks = ceil_div(H, GEMM_BK);
-    p.part_blocks = LOGIT_PART_BLOCKS;
+    p.part_blocks = ceil_div(p.kblocks, ceil_div(p.kblocks, LOGIT_PART_BLOCKS));
     p.splits = 1;
     p.group_m = vocab_group(H);
     p.target = rp.packed_target;
@@ -337,7 +336,7 @@ int moe_vocab_loss(int32_t T, int32_t H, int32_t V, const moe_bf16 *hidden, cons
     p.ld_stats = T;
     p.target_logit = at<float>(ws, L.logit);
     p.status = status;
-    GLR_LAUNCH(KID_VOCAB_LOGITS, launch_pair_gemm(few ? PG_STATS_FEW : PG_STATS, false, false, p, ceil_div(T, 256) * L.ntiles,
+    GLR_LAUNCH(KID_VOCAB_LOGITS, launch_pair_gemm(few ? PG_STATS_FEW : PG_STATS, PP_LOGITS, p, ceil_div(T, 256) * L.ntiles,
                                                    s));
     GLR_LAUNCH(KID_VOCAB_JOIN, launch_vocab_join(p.stats, L.nstats, T, p.target_logit, meta, rp.row_of, T, loss, lse,
                                                  s));
@@ -405,7 +404,6 @@ int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hid
     pz.T = T;
     pz.meta = meta;
     pz.m_from_rows = 1;
-    pz.nseg = 1;
     pz.kblocks = pz.part_blocks = ceil_div(H, GEMM_BK);
     pz.splits = 1;
     pz.group_m = vocab_group(H);
@@ -423,7 +421,6 @@ int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hid
     px.meta = meta;
     px.m_from_rows = 1;
     px.N = H;
-    px.nseg = 1;
     px.splits = L.splits;
     px.group_m = 1;
     px.out_rows = L.splits * L.split_rows;
@@ -441,7 +438,6 @@ int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hid
     pw.k_from_rows = 1;
     pw.part_blocks = ceil_div(T, GEMM_BK);
     pw.N = H;
-    pw.nseg = 1;
     pw.splits = 1;
     pw.group_m = 1;
     pw.out_rows = V;
@@ -453,14 +449,14 @@ int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hid
         pz.n0 = v0;
         pz.b_off[0] = v0;
         GLR_LAUNCH(KID_VOCAB_DLOGITS,
-                   launch_pair_gemm(PG_DLOGITS, false, false, pz, m_tiles * ceil_div(n, 256), s));
+                   launch_pair_gemm(PG_DLOGITS, PP_LOGITS, pz, m_tiles * ceil_div(n, 256), s));
         px.kblocks = px.part_blocks = ceil_div(n, GEMM_BK);
         px.b_off[0] = v0;
         px.accumulate = v0 > 0;
-        GLR_LAUNCH(KID_VOCAB_DX, launch_pair_gemm(PG_PARTIAL, false, true, px, m_tiles * h_tiles * L.splits, s));
+        GLR_LAUNCH(KID_VOCAB_DX, launch_pair_gemm(PG_PARTIAL, PP_DX, px, m_tiles * h_tiles * L.splits, s));
         pw.M = n;
         pw.out_row0 = v0;
-        GLR_LAUNCH(KID_VOCAB_DW, launch_pair_gemm(PG_BF16, true, true, pw, ceil_div(n, 256) * h_tiles, s));
+        GLR_LAUNCH(KID_VOCAB_DW, launch_pair_gemm(PG_BF16, PP_DW, pw, ceil_div(n, 256) * h_tiles, s));
     }
     GLR_LAUNCH(KID_VOCAB_DX, launch_vocab_dx_join(part, L.splits, (long long)L.split_rows * H, meta, rp.packed_of, T, H,
                                                   d_hidden, s));
@@ -521,18 +517,17 @@ int moe_route_backward(const moe_cfg *cfg, const moe_bf16 *hidden, const float *
         return MOE_ERR_CUDA;
     p.M = c.T;
     p.N = c.H;
-    p.nseg = 3;
     p.kblocks = p.part_blocks = c.E / GEMM_BK;
-    p.a_off[0] = c.T;              // middle x high
-    p.b_off[1] = c.E;              // high x middle
-    p.splits = 1;                  // (third segment: high x high)
+    p.a_off[1] = c.T;              // the middle parts
+    p.b_off[1] = c.E;
+    p.splits = 1;
     p.group_m = 1;
     p.out_rows = c.T;
     p.out_cols = c.H;
     p.status = status;
     if (d_hidden_add && !make_map_bf16(&p.tmHidden, d_hidden_add, c.T, c.H, 64, 32))
         return MOE_ERR_CUDA;
-    GLR_LAUNCH(KID_ROUTE_BWD_DX, launch_pair_gemm(d_hidden_add ? PG_BF16_ADD : PG_BF16, false, true, p, ceil_div(c.T, 256) * h_tiles, s));
+    GLR_LAUNCH(KID_ROUTE_BWD_DX, launch_pair_gemm(d_hidden_add ? PG_BF16_ADD : PG_BF16, PP_DX_PARTS, p, ceil_div(c.T, 256) * h_tiles, s));
     // dW = dL^T hidden, exact products: low, middle, high part of dL
     float *part = at<float>(ws, L.part);
     memset(&p, 0, sizeof(p));
@@ -542,18 +537,17 @@ int moe_route_backward(const moe_cfg *cfg, const moe_bf16 *hidden, const float *
         return MOE_ERR_CUDA;
     p.M = c.E;
     p.N = c.H;
-    p.nseg = 3;
     p.kblocks = ceil_div(c.T, GEMM_BK);
     p.part_blocks = ROUTE_DW_BLOCKS;
-    p.a_off[0] = 2 * c.T;
     p.a_off[1] = c.T;
+    p.a_off[2] = 2 * c.T;
     p.splits = L.splits;
     p.group_m = 1;
     p.out_rows = 256 * L.splits;
     p.out_cols = c.H;
     p.split_rows = 256;
     p.status = status;
-    GLR_LAUNCH(KID_ROUTE_BWD_DW, launch_pair_gemm(PG_PARTIAL, true, true, p, h_tiles * L.splits, s));
+    GLR_LAUNCH(KID_ROUTE_BWD_DW, launch_pair_gemm(PG_PARTIAL, PP_DW_PARTS, p, h_tiles * L.splits, s));
     GLR_LAUNCH(KID_ROUTE_BWD_DW, launch_sum_splits(part, L.splits, 256ll * c.H, (long long)c.E * c.H, dW_router, s));
     set_last_launches(launches);
     return MOE_OK;

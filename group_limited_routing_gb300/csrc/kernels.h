@@ -365,10 +365,10 @@ struct PairGemmParams {
     int m_from_rows;          // M = meta->rows
     int k_from_rows;          // K = meta->rows
     int M, N;
-    int nseg, kblocks;        // K = nseg segments of kblocks blocks of 64
-    int a_off[3], b_off[3];   // per segment: rows added to the operand's row coordinate
-    int splits;               // K range cut among this many units (inside every segment)
-    int part_blocks;          // blocks per segment and accumulator (STATS, PARTIAL; else at least kblocks)
+    int kblocks;              // K in blocks of 64
+    int a_off[3], b_off[2];   // rows added to the operand's row coordinate (of each part)
+    int splits;               // K range cut among this many units
+    int part_blocks;          // K blocks per accumulator (STATS, PARTIAL; else at least kblocks)
     int group_m;              // tiles run m-fastest within groups of this many m-tiles
     int out_row0;             // row of the output map where row 0 goes
     int out_rows, out_cols;   // the output map's extent
@@ -383,7 +383,12 @@ struct PairGemmParams {
     const float *lse, *weight; // per packed row
     int *status;
 };
-cudaError_t launch_pair_gemm(PairEpilogue epi, bool a_mn, bool b_mn, const PairGemmParams &p, int max_units,
+// The operands of a product: rows of K (A, B as nn.Linear has them), B as rows
+// of N, both as rows of M and N (a gradient's transposed operand); with parts,
+// the fp32 operands as bf16 parts stacked along their rows (A and B in two each;
+// A in three).
+enum PairProduct { PP_LOGITS = 0, PP_DX = 1, PP_DW = 2, PP_DX_PARTS = 3, PP_DW_PARTS = 4 };
+cudaError_t launch_pair_gemm(PairEpilogue epi, PairProduct product, const PairGemmParams &p, int max_units,
                              cudaStream_t s);
 
 // ---- vocabulary loss (vocab.cu) -----------------------------------------------

@@ -20,8 +20,7 @@
 // parts in registers, rounding to nearest.
 //
 // Roles (320 threads): warp 0 lane 0 loads, warp 1 lane 0 of the even CTA
-// issues the MMAs (of the odd one, forwards its epilogue's arrivals to the
-// even one), warps 2..9 run the epilogue: TMEM lanes 32 (w % 4) .. + 31, the
+// issues the MMAs, warps 2..9 run the epilogue: TMEM lanes 32 (w % 4) .. + 31, the
 // tile's left or right 128 columns.
 // Every wait is bounded; when one runs out, every role leaves its loop, copies
 // in flight are waited for (bounded), TMEM is freed and the status word gets
@@ -58,15 +57,19 @@ constexpr bool IS_STATS = EPI == PG_STATS || EPI == PG_STATS_FEW;
 // from memory: a stage holds those rows of A only, and the shared memory this
 // frees goes to a deeper ring of B.  The MMA still reads 128 rows per CTA; the
 // rest alias the bytes behind and reach accumulator rows that nobody reads.
-template <int EPI>
+// SPLIT: an fp32 operand as bf16 parts.  A stage then holds the K block of
+// every part once, SPLIT parts of A and 4 - SPLIT of B, and the MMA issuer forms
+// the products of parts from it (2: middle x high, high x middle, high x high;
+// 3: low, middle, high x B): four loads for three products.
+template <int EPI, int SPLIT>
 struct PgCfg {
     static constexpr bool FEW = EPI == PG_STATS_FEW;
     static constexpr int A_ROWS = FEW ? PAIR_FEW_ROWS : 128;
     static constexpr int A_BYTES = A_ROWS * GEMM_BK * 2;
-    static constexpr int STAGE_BYTES = A_BYTES + PG_B_BYTES;
+    static constexpr int STAGE_BYTES = SPLIT ? 4 * PG_B_BYTES : A_BYTES + PG_B_BYTES;
     static constexpr int BUFS = IS_STATS<EPI> ? 0 : EPI == PG_BF16_ADD ? 3 : 1;
-    static constexpr int STAGES = FEW ? 11 : 7 - BUFS;
     static constexpr int STAGING = BUFS * PG_EPI_WARPS * 4096;
+    static constexpr int STAGES = (230400 - STAGING) / STAGE_BYTES;
     static constexpr int NBARS = 2 * STAGES + 2 * PG_SLOTS + 1 + PG_EPI_WARPS;
     static constexpr int SMEM = STAGES * STAGE_BYTES + STAGING + 1024 /*align*/ + NBARS * 8 + 16;
     static_assert(SMEM <= 232448, "more than 227 KB of shared memory");
@@ -87,11 +90,10 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// One unit of work: a tile and its K blocks (the same range of every segment),
-// in parts of at most p.part_blocks blocks per segment.
+// One unit of work: a tile and its K blocks, in parts of at most p.part_blocks.
 struct Unit {
     int m0, n0, nt, split;
-    int k0, k1;              // blocks of each segment
+    int k0, k1;
     int parts;
 };
 
@@ -309,10 +311,10 @@ __device__ __forceinline__ void bf16_box(uint32_t tacc, bool empty, float scale,
     }
 }
 
-template <int EPI, bool A_MN, bool B_MN>
+template <int EPI, bool A_MN, bool B_MN, int SPLIT>
 __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_constant__ PairGemmParams p)
 {
-    using C = PgCfg<EPI>;
+    using C = PgCfg<EPI, SPLIT>;
     constexpr uint32_t IDESC = idesc_bf16_f32(PG_BM, PG_BN, A_MN, B_MN);
     extern __shared__ uint8_t dsmem[];
     const uint32_t raw = smem_u32(dsmem);
@@ -341,8 +343,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
         }
         for (int a = 0; a < PG_SLOTS; ++a) {
             mbar_init(tfull0 + 8u * a, 1);
-            // this CTA's epilogue warps; the leader's also counts the peer's forwarder
-            mbar_init(tempty0 + 8u * a, PG_EPI_WARPS + (leader ? 1 : 0));
+            mbar_init(tempty0 + 8u * a, 2 * PG_EPI_WARPS);    // (the leader's: both CTAs' epilogue warps)
         }
         mbar_init(fin_bar, 1);
         for (int w = 0; w < PG_EPI_WARPS; ++w)
@@ -380,41 +381,42 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
             for (int u = pair; ok && u < sh.units; u += npairs) {
                 const Unit t = unit_of(p, sh, u);
                 const int m = t.m0 + rank * 128, n = t.n0 + rank * 128;
-                for (int part = 0; part < t.parts; ++part) {
-                    const int kp = t.k0 + part * p.part_blocks, ke = min(kp + p.part_blocks, t.k1);
-                    for (int seg = 0; ok && seg < p.nseg; ++seg) {
-                        for (int kb = kp; kb < ke; ++kb) {
-                            if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) {
-                                ok = false;
-                                break;
-                            }
-                            const uint32_t sA = base + stage * C::STAGE_BYTES, sB = sA + C::A_BYTES;
-                            if (leader)
-                                mbar_arrive_expect_tx(full_bar(stage), C::FEW ? C::A_BYTES + 2 * PG_B_BYTES
-                                                                              : 2 * C::STAGE_BYTES);
-                            const uint32_t fb = full_leader0 + 8u * stage;
-                            const int k = kb * GEMM_BK;
-                            if (A_MN) {
+                for (int kb = t.k0; kb < t.k1; ++kb) {
+                    if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    uint32_t to = base + stage * C::STAGE_BYTES;
+                    if (leader)
+                        mbar_arrive_expect_tx(full_bar(stage),
+                                              C::FEW ? C::A_BYTES + 2 * PG_B_BYTES : 2 * C::STAGE_BYTES);
+                    const uint32_t fb = full_leader0 + 8u * stage;
+                    const int k = kb * GEMM_BK;
 #pragma unroll
-                                for (int q = 0; q < 2; ++q)
-                                    tma_load_2d_pair(sA + q * PG_ATOM, ma, fb, m + q * 64, k + p.a_off[seg]);
-                            } else if (!C::FEW || leader) {
-                                tma_load_2d_pair(sA, ma, fb, k, m + p.a_off[seg]);
-                            }
-                            if (B_MN) {
+                    for (int i = 0; i < (SPLIT ? SPLIT : 1); ++i, to += C::A_BYTES) {
+                        if (A_MN) {
 #pragma unroll
-                                for (int q = 0; q < 2; ++q)
-                                    tma_load_2d_pair(sB + q * PG_ATOM, mb, fb, n + q * 64, k + p.b_off[seg]);
-                            } else {
-                                tma_load_2d_pair(sB, mb, fb, k, n + p.b_off[seg]);
-                            }
-                            issued |= 1u << stage;
-                            issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-                            if (++stage == C::STAGES) {
-                                stage = 0;
-                                phase ^= 1u;
-                            }
+                            for (int q = 0; q < 2; ++q)
+                                tma_load_2d_pair(to + q * PG_ATOM, ma, fb, m + q * 64, k + p.a_off[i]);
+                        } else if (!C::FEW || leader) {
+                            tma_load_2d_pair(to, ma, fb, k, m + p.a_off[i]);
                         }
+                    }
+#pragma unroll
+                    for (int i = 0; i < (SPLIT ? 4 - SPLIT : 1); ++i, to += PG_B_BYTES) {
+                        if (B_MN) {
+#pragma unroll
+                            for (int q = 0; q < 2; ++q)
+                                tma_load_2d_pair(to + q * PG_ATOM, mb, fb, n + q * 64, k + p.b_off[i]);
+                        } else {
+                            tma_load_2d_pair(to, mb, fb, k, n + p.b_off[i]);
+                        }
+                    }
+                    issued |= 1u << stage;
+                    issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+                    if (++stage == C::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
                     }
                 }
             }
@@ -438,31 +440,40 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
                 const Unit t = unit_of(p, sh, u);
                 for (int part = 0; ok && part < t.parts; ++part) {
                     const int kp = t.k0 + part * p.part_blocks, ke = min(kp + p.part_blocks, t.k1);
-                    const int nkb = (ke - kp) * p.nseg;
                     const uint32_t slot = ctr % PG_SLOTS, par = (ctr / PG_SLOTS) & 1u;
-                    // (the peer's forwarder arrives here across the pair)
+                    // (the peer's epilogue warps arrive here across the pair)
                     if (!mbar_wait_cluster(tempty0 + 8u * slot, par ^ 1u, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t d = tmem + slot * 256;
-                    for (int kb = 0; kb < nkb; ++kb) {
+                    for (int kb = kp; kb < ke; ++kb) {
                         if (!mbar_wait(full_bar(stage), phase, abort_flag)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t sA = base + stage * C::STAGE_BYTES, sB = sA + C::A_BYTES;
+                        const uint32_t sA = base + stage * C::STAGE_BYTES;
+                        const uint32_t sB = sA + (SPLIT ? SPLIT : 1) * C::A_BYTES;
+                        constexpr int PRODUCTS = SPLIT ? 3 : 1;
 #pragma unroll
-                        for (int kk = 0; kk < GEMM_BK / 16; ++kk)
-                            // 16 K: 32 B along a K-major row, 2048 B (two 8-row atoms) of an MN-major operand
-                            umma_bf16_pair(d,
-                                           A_MN ? sdesc_mnmajor_sw128(sA + kk * 2048, PG_ATOM)
-                                                : sdesc_kmajor_sw128(sA + kk * 32),
-                                           B_MN ? sdesc_mnmajor_sw128(sB + kk * 2048, PG_ATOM)
-                                                : sdesc_kmajor_sw128(sB + kk * 32),
-                                           IDESC, (kb > 0 || kk > 0) ? 1u : 0u);
+                        for (int kk = 0; kk < GEMM_BK / 16; ++kk) {
+#pragma unroll
+                            for (int j = 0; j < PRODUCTS; ++j) {
+                                // the smallest product of parts first
+                                const int ai = SPLIT == 3 ? 2 - j : SPLIT == 2 ? (j == 0 ? 1 : 0) : 0;
+                                const int bi = SPLIT == 2 ? (j == 1 ? 1 : 0) : 0;
+                                const uint32_t a = sA + ai * C::A_BYTES, b = sB + bi * PG_B_BYTES;
+                                // 16 K: 32 B along a K-major row, 2048 B (two 8-row atoms) of an MN-major operand
+                                umma_bf16_pair(d,
+                                               A_MN ? sdesc_mnmajor_sw128(a + kk * 2048, PG_ATOM)
+                                                    : sdesc_kmajor_sw128(a + kk * 32),
+                                               B_MN ? sdesc_mnmajor_sw128(b + kk * 2048, PG_ATOM)
+                                                    : sdesc_kmajor_sw128(b + kk * 32),
+                                               IDESC, (kb > kp || kk > 0 || j > 0) ? 1u : 0u);
+                            }
+                        }
                         umma_commit_pair(empty_bar(stage), 0x3);      // both CTAs' stage is read
                         if (++stage == C::STAGES) {
                             stage = 0;
@@ -477,22 +488,6 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
             }
             umma_commit_pair(fin_bar, 0x1);
             mbar_drain(fin_bar, 0);
-        } else if (lane == 0) {
-            // ------------------------------------------- the peer's forwarder
-            const uint32_t tempty_leader = mapa_shared(tempty0, 0);
-            uint32_t ctr = 0;
-            bool ok = true;
-            for (int u = pair; ok && u < sh.units; u += npairs) {
-                const Unit t = unit_of(p, sh, u);
-                for (int part = 0; part < t.parts; ++part, ++ctr) {
-                    const uint32_t slot = ctr % PG_SLOTS, par = (ctr / PG_SLOTS) & 1u;
-                    if (!mbar_wait(tempty0 + 8u * slot, par, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_arrive_cluster(tempty_leader + 8u * slot);
-                }
-            }
         }
     } else {
         // ------------------------------------------------------------ epilogue
@@ -515,12 +510,13 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
         auto tacc = [&]() {
             return tmem + ((uint32_t)(quad * 32) << 16) + (ctr % PG_SLOTS) * 256 + half * PG_HALF;
         };
-        // gives the accumulator back (the peer's forwarder passes it on to the leader)
+        // gives the accumulator back to the MMA issuer, in the even CTA
+        const uint32_t tempty_leader = mapa_shared(tempty0, 0);
         auto release = [&]() {
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(tempty0 + 8u * (ctr % PG_SLOTS));
+                mbar_arrive_cluster(tempty_leader + 8u * (ctr % PG_SLOTS));
             ++ctr;
         };
         // the addend's two boxes of unit u
@@ -643,10 +639,10 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
         atomicOr(p.status, ST_TIMEOUT);
 }
 
-template <int EPI, bool A_MN, bool B_MN>
+template <int EPI, bool A_MN, bool B_MN, int SPLIT = 0>
 cudaError_t launch_one(const PairGemmParams &p, int max_units, cudaStream_t s)
 {
-    auto kernel = pair_gemm_kernel<EPI, A_MN, B_MN>;
+    auto kernel = pair_gemm_kernel<EPI, A_MN, B_MN, SPLIT>;
     static int configured_device = -1;
     static int max_clusters = 0;
     int dev = 0;
@@ -660,12 +656,12 @@ cudaError_t launch_one(const PairGemmParams &p, int max_units, cudaStream_t s)
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.blockDim = dim3(PG_THREADS);
-    cfg.dynamicSmemBytes = PgCfg<EPI>::SMEM;
+    cfg.dynamicSmemBytes = PgCfg<EPI, SPLIT>::SMEM;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     if (configured_device != dev) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PgCfg<EPI>::SMEM);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PgCfg<EPI, SPLIT>::SMEM);
         if (e != cudaSuccess)
             return e;
         cfg.gridDim = dim3(2);
@@ -686,25 +682,37 @@ cudaError_t launch_one(const PairGemmParams &p, int max_units, cudaStream_t s)
 }  // namespace
 
 // max_units: tiles times splits if every row counts
-cudaError_t launch_pair_gemm(PairEpilogue epi, bool a_mn, bool b_mn, const PairGemmParams &p, int max_units,
+cudaError_t launch_pair_gemm(PairEpilogue epi, PairProduct product, const PairGemmParams &p, int max_units,
                              cudaStream_t s)
 {
-    if (epi == PG_STATS && !a_mn && !b_mn)
-        return launch_one<PG_STATS, false, false>(p, max_units, s);
-    if (epi == PG_STATS_FEW && !a_mn && !b_mn)
-        return launch_one<PG_STATS_FEW, false, false>(p, max_units, s);
-    if (epi == PG_DLOGITS && !a_mn && !b_mn)
-        return launch_one<PG_DLOGITS, false, false>(p, max_units, s);
-    if (epi == PG_PARTIAL && !a_mn && b_mn)
-        return launch_one<PG_PARTIAL, false, true>(p, max_units, s);
-    if (epi == PG_PARTIAL && a_mn && b_mn)
-        return launch_one<PG_PARTIAL, true, true>(p, max_units, s);
-    if (epi == PG_BF16 && !a_mn && b_mn)
-        return launch_one<PG_BF16, false, true>(p, max_units, s);
-    if (epi == PG_BF16_ADD && !a_mn && b_mn)
-        return launch_one<PG_BF16_ADD, false, true>(p, max_units, s);
-    if (epi == PG_BF16 && a_mn && b_mn)
-        return launch_one<PG_BF16, true, true>(p, max_units, s);
+    switch (product) {
+    case PP_LOGITS:
+        if (epi == PG_STATS)
+            return launch_one<PG_STATS, false, false>(p, max_units, s);
+        if (epi == PG_STATS_FEW)
+            return launch_one<PG_STATS_FEW, false, false>(p, max_units, s);
+        if (epi == PG_DLOGITS)
+            return launch_one<PG_DLOGITS, false, false>(p, max_units, s);
+        break;
+    case PP_DX:
+        if (epi == PG_PARTIAL)
+            return launch_one<PG_PARTIAL, false, true>(p, max_units, s);
+        break;
+    case PP_DW:
+        if (epi == PG_BF16)
+            return launch_one<PG_BF16, true, true>(p, max_units, s);
+        break;
+    case PP_DX_PARTS:
+        if (epi == PG_BF16)
+            return launch_one<PG_BF16, false, true, 2>(p, max_units, s);
+        if (epi == PG_BF16_ADD)
+            return launch_one<PG_BF16_ADD, false, true, 2>(p, max_units, s);
+        break;
+    case PP_DW_PARTS:
+        if (epi == PG_PARTIAL)
+            return launch_one<PG_PARTIAL, true, true, 3>(p, max_units, s);
+        break;
+    }
     return cudaErrorInvalidValue;
 }
 
