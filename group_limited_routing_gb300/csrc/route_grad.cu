@@ -28,15 +28,6 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// sum of the K parts of one logit, in part order
-__device__ __forceinline__ float logit_at(const float *logits, int nparts, long long stride, size_t at)
-{
-    float v = logits[at];
-    for (int q = 1; q < nparts; ++q)
-        v += logits[at + q * stride];
-    return v;
-}
-
 }  // namespace
 
 // One warp per token; a lane holds EPL = E / 32 neighbouring experts.
@@ -59,34 +50,47 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const float *__restrict
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
         f[i] = d_aux ? (float)counts[lane * EPL + i] / ((float)k * (float)T) : 0.0f;
-    for (int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); t < T; t += warps) {
-        const float *row = logits + (size_t)t * E;
-        float L[EPL], ds[EPL], s[EPL], slope[EPL];
-        int e = -1;
-        if (lane < k)
-            e = idx[(size_t)t * k + lane];
+    // a token's logits, chosen experts and their gradients, loaded a token ahead
+    float4 ahead[EPL / 4];
+    int e_ahead = -1;
+    float dw_ahead = 0.0f;
+    auto fetch = [&](int t) {
+        if (t >= T)
+            return;
+        const float *row = logits + (size_t)t * E + lane * EPL;
 #pragma unroll
-        for (int i = 0; i < EPL; i += 4) {
-            const float4 q = *reinterpret_cast<const float4 *>(row + lane * EPL + i);
-            L[i] = q.x; L[i + 1] = q.y; L[i + 2] = q.z; L[i + 3] = q.w;
-        }
+        for (int i = 0; i < EPL / 4; ++i)
+            ahead[i] = reinterpret_cast<const float4 *>(row)[i];
         for (int part = 1; part < nparts; ++part)
 #pragma unroll
-            for (int i = 0; i < EPL; i += 4) {
-                const float4 q = *reinterpret_cast<const float4 *>(row + part * stride + lane * EPL + i);
-                L[i] += q.x; L[i + 1] += q.y; L[i + 2] += q.z; L[i + 3] += q.w;
+            for (int i = 0; i < EPL / 4; ++i) {
+                const float4 q = reinterpret_cast<const float4 *>(row + part * stride)[i];
+                ahead[i].x += q.x; ahead[i].y += q.y; ahead[i].z += q.z; ahead[i].w += q.w;
             }
-        // lane j < k: the chosen expert j
-        float dw = 0.0f, sj = 0.0f;
         if (lane < k) {
-            if (e < 0 || e >= E) {
-                atomicOr(status, ST_BAD_INDEX);
-                e = -1;
-            } else {
-                dw = d_w[(size_t)t * k + lane];
-                sj = router_sigmoid(logit_at(row, nparts, stride, e));
-            }
+            e_ahead = idx[(size_t)t * k + lane];
+            dw_ahead = d_w[(size_t)t * k + lane];
         }
+    };
+    float *mine = scatter[threadIdx.x >> 5];
+    int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    fetch(t);
+    for (; t < T; t += warps) {
+        float L[EPL], ds[EPL], s[EPL], slope[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL / 4; ++i) {
+            L[4 * i] = ahead[i].x; L[4 * i + 1] = ahead[i].y; L[4 * i + 2] = ahead[i].z; L[4 * i + 3] = ahead[i].w;
+        }
+        // lane j < k: the chosen expert j
+        int e = e_ahead;
+        float dw = dw_ahead;
+        fetch(t + warps);
+        if (lane < k && (e < 0 || e >= E)) {
+            atomicOr(status, ST_BAD_INDEX);
+            e = -1;
+        }
+        if (e < 0)
+            dw = 0.0f;
         float Z = 0.0f, F = 0.0f, zero = 0.0f;          // zero: 0 unless a logit is not finite
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
@@ -99,12 +103,18 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const float *__restrict
         }
         if (!__all_sync(0xffffffffu, zero == 0.0f) && lane == 0)
             atomicOr(status, ST_NONFINITE);
+        // scores to the lanes whose expert they are, through shared memory; the
+        // gradients back the same way
+#pragma unroll
+        for (int i = 0; i < EPL; i += 4)
+            *reinterpret_cast<float4 *>(mine + lane * EPL + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+        __syncwarp();
+        const float sj = e >= 0 ? mine[e] : 0.0f;
         const float D = warp_sum(sj) + eps;
         const float m = __fdividef(warp_sum(dw * sj), D);
         float dsj = __fdividef(rsf, D) * (dw - m);
-        // to the lanes that hold the experts, through shared memory; an id that
-        // a token names more than once (never the router's) adds up in the
-        // first lane that names it
+        // (an id that a token names more than once, never the router's, adds up
+        // in the first lane that names it)
         const unsigned same = __match_any_sync(0xffffffffu, e);
         const bool first = e >= 0 && __ffs(same) - 1 == lane;
         if (__any_sync(0xffffffffu, e >= 0 && !first)) {
@@ -116,7 +126,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const float *__restrict
             }
             dsj = sum;
         }
-        float *mine = scatter[threadIdx.x >> 5];
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < EPL; i += 4)
             *reinterpret_cast<float4 *>(mine + lane * EPL + i) = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -180,7 +190,7 @@ cudaError_t launch_route_grad(const float *logits, int nparts, const int32_t *id
                               const float *d_aux, int T, int E, int k, float rsf, float eps, uint16_t *parts,
                               int *status, cudaStream_t s)
 {
-    const int want = (T + 7) / 8, most = 152 * 8;
+    const int want = (T + 7) / 8, most = 152 * 5;      // (what the SMs hold at once)
     const dim3 grid(want < most ? want : most);
     const cudaError_t e = E == 256 ? launch_pdl(route_grad_kernel<8>, grid, dim3(256), 0, s, logits, nparts, idx, d_w, counts,
                                                 d_aux, T, k, rsf, eps, parts, status)

@@ -91,6 +91,9 @@ def _stream(device) -> int:
 
 
 def _need(t: torch.Tensor, name: str, dtype, shape, device) -> int:
+    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device and
+            t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a tensor" % name)
     if t.dtype != dtype:
