@@ -72,6 +72,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = False) -> ctypes.CDLL:
     """Load libglr_moe.so (building it first only if asked)."""
     global _handle
+    if _handle is not None:
+        return _handle
     with _lock:
         if _handle is not None:
             return _handle

@@ -52,10 +52,11 @@ int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 // K splits of a product with few output tiles: the number that finishes
 // soonest when a pair takes units of kblocks / splits K blocks one after the
 // other, each with an epilogue that costs about EPILOGUE_BLOCKS more, and every
-// split's sums (`elements` of them) are written and read once more.  One K block
+// split's sums (`elements` of them) are written and read once more by a kernel
+// of its own (SUM_BLOCKS).  One K block
 // takes a pair 0.27 us, in which HBM moves 450,000 fp32 values.  The number
 // depends on the shape alone, so results do not change with the device's load.
-constexpr int EPILOGUE_BLOCKS = 4;
+constexpr int EPILOGUE_BLOCKS = 4, SUM_BLOCKS = 10;
 constexpr double ELEMENTS_PER_BLOCK = 450e3;
 
 int choose_splits(int tiles, int kblocks, double elements, int max_splits, int min_blocks)
@@ -65,7 +66,7 @@ int choose_splits(int tiles, int kblocks, double elements, int max_splits, int m
     for (int n = 1; n <= max_splits && (n == 1 || kblocks / n >= min_blocks); ++n) {
         const double cost = (double)ceil_div((long long)tiles * n, PAIRS) *
                                 (ceil_div(kblocks, n) + EPILOGUE_BLOCKS) +
-                            2.0 * n * elements / ELEMENTS_PER_BLOCK;
+                            (n > 1 ? SUM_BLOCKS : 0) + 2.0 * n * elements / ELEMENTS_PER_BLOCK;
         if (n == 1 || cost < best_cost) {
             best = n;
             best_cost = cost;
@@ -167,7 +168,7 @@ RouteBwdLayout route_bwd_layout(const moe_cfg &c)
     L.split = take(3ull * c.E * c.H * 2);
     L.parts = take(3ull * c.T * c.E * 2);
     L.splits = choose_splits(ceil_div(c.H, 256), 3 * ceil_div(c.T, GEMM_BK), 256.0 * c.H, 64, 3);
-    L.part = take(4ull * L.splits * 256 * c.H);
+    L.part = take(L.splits > 1 ? 4ull * L.splits * 256 * c.H : 0);
     L.total = off;
     return L;
 }
@@ -533,7 +534,8 @@ int moe_route_backward(const moe_cfg *cfg, const moe_bf16 *hidden, const float *
     memset(&p, 0, sizeof(p));
     if (!make_map_bf16(&p.tmA, parts, 3ull * c.T, c.E, 64, GEMM_BK) ||
         !make_map_bf16(&p.tmB, hidden, c.T, c.H, 64, GEMM_BK) ||
-        !make_map_f32(&p.tmOut, part, 256ull * L.splits, c.H, 32, 32))
+        !(L.splits == 1 ? make_map_f32(&p.tmOut, dW_router, c.E, c.H, 32, 32)
+                        : make_map_f32(&p.tmOut, part, 256ull * L.splits, c.H, 32, 32)))
         return MOE_ERR_CUDA;
     p.M = c.E;
     p.N = c.H;
@@ -543,12 +545,13 @@ int moe_route_backward(const moe_cfg *cfg, const moe_bf16 *hidden, const float *
     p.a_off[2] = 2 * c.T;
     p.splits = L.splits;
     p.group_m = 1;
-    p.out_rows = 256 * L.splits;
+    p.out_rows = L.splits == 1 ? c.E : 256 * L.splits;
     p.out_cols = c.H;
     p.split_rows = 256;
     p.status = status;
     GLR_LAUNCH(KID_ROUTE_BWD_DW, launch_pair_gemm(PG_PARTIAL, PP_DW_PARTS, p, h_tiles * L.splits, s));
-    GLR_LAUNCH(KID_ROUTE_BWD_DW, launch_sum_splits(part, L.splits, 256ll * c.H, (long long)c.E * c.H, dW_router, s));
+    if (L.splits > 1)
+        GLR_LAUNCH(KID_ROUTE_BWD_DW, launch_sum_splits(part, L.splits, 256ll * c.H, (long long)c.E * c.H, dW_router, s));
     set_last_launches(launches);
     return MOE_OK;
 }

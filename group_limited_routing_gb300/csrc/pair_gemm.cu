@@ -57,16 +57,19 @@ constexpr bool IS_STATS = EPI == PG_STATS || EPI == PG_STATS_FEW;
 // from memory: a stage holds those rows of A only, and the shared memory this
 // frees goes to a deeper ring of B.  The MMA still reads 128 rows per CTA; the
 // rest alias the bytes behind and reach accumulator rows that nobody reads.
-// SPLIT: an fp32 operand as bf16 parts.  A stage then holds the K block of
-// every part once, SPLIT parts of A and 4 - SPLIT of B, and the MMA issuer forms
-// the products of parts from it (2: middle x high, high x middle, high x high;
-// 3: low, middle, high x B): four loads for three products.
+// SPLIT: fp32 operands as bf16 parts, SPLIT of A and 4 - SPLIT of B, of which
+// three products are formed: four loads for three products.  A stage is then one
+// part's K block (16 KB), released by the last product that reads it; a stage of
+// all four left the tensor core waiting for memory (two fit beside the boxes).
+//   2: the parts in order A middle, B high, A high, B middle, and the products
+//      middle x high, high x high, high x middle
+//   3: B, A low, A middle, A high, and each A x B as its A arrives
 template <int EPI, int SPLIT>
 struct PgCfg {
     static constexpr bool FEW = EPI == PG_STATS_FEW;
     static constexpr int A_ROWS = FEW ? PAIR_FEW_ROWS : 128;
     static constexpr int A_BYTES = A_ROWS * GEMM_BK * 2;
-    static constexpr int STAGE_BYTES = SPLIT ? 4 * PG_B_BYTES : A_BYTES + PG_B_BYTES;
+    static constexpr int STAGE_BYTES = SPLIT ? PG_B_BYTES : A_BYTES + PG_B_BYTES;
     static constexpr int BUFS = IS_STATS<EPI> ? 0 : EPI == PG_BF16 || EPI == PG_BF16_ADD ? 2 : 1;
     static constexpr int STAGING = BUFS * PG_EPI_WARPS * 4096;
     static constexpr int STAGES = (230400 - STAGING) / STAGE_BYTES;
@@ -396,36 +399,38 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
             for (int u = pair; ok && u < sh.units; u += npairs) {
                 const Unit t = unit_of(p, sh, u);
                 const int m = t.m0 + rank * 128, n = t.n0 + rank * 128;
-                for (int kb = t.k0; kb < t.k1; ++kb) {
+                constexpr int LOADS = SPLIT ? 4 : 1;          // stages of a K block
+                for (int i = 0; ok && i < (t.k1 - t.k0) * LOADS; ++i) {
                     if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) {
                         ok = false;
                         break;
                     }
-                    uint32_t to = base + stage * C::STAGE_BYTES;
+                    const uint32_t to = base + stage * C::STAGE_BYTES;
                     if (leader)
                         mbar_arrive_expect_tx(full_bar(stage),
                                               C::FEW ? C::A_BYTES + 2 * PG_B_BYTES : 2 * C::STAGE_BYTES);
                     const uint32_t fb = full_leader0 + 8u * stage;
-                    const int k = kb * GEMM_BK;
-#pragma unroll
-                    for (int i = 0; i < (SPLIT ? SPLIT : 1); ++i, to += C::A_BYTES) {
-                        if (A_MN) {
-#pragma unroll
-                            for (int q = 0; q < 2; ++q)
-                                tma_load_2d_pair(to + q * PG_ATOM, ma, fb, m + q * 64, k + p.a_off[i]);
-                        } else if (!C::FEW || leader) {
-                            tma_load_2d_pair(to, ma, fb, k, m + p.a_off[i]);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < (SPLIT ? 4 - SPLIT : 1); ++i, to += PG_B_BYTES) {
-                        if (B_MN) {
+                    const int k = (t.k0 + i / LOADS) * GEMM_BK;
+                    auto load = [&](const CUtensorMap *map, bool mn_major, int mn, int off, uint32_t dst) {
+                        if (mn_major) {
 #pragma unroll
                             for (int q = 0; q < 2; ++q)
-                                tma_load_2d_pair(to + q * PG_ATOM, mb, fb, n + q * 64, k + p.b_off[i]);
+                                tma_load_2d_pair(dst + q * PG_ATOM, map, fb, mn + q * 64, k + off);
                         } else {
-                            tma_load_2d_pair(to, mb, fb, k, n + p.b_off[i]);
+                            tma_load_2d_pair(dst, map, fb, k, mn + off);
                         }
+                    };
+                    if (SPLIT) {
+                        const int j = i % LOADS;
+                        const bool is_b = SPLIT == 2 ? (j & 1) : j == 0;
+                        if (is_b)
+                            load(mb, B_MN, n, p.b_off[SPLIT == 2 ? j >> 1 : 0], to);
+                        else
+                            load(ma, A_MN, m, p.a_off[SPLIT == 2 ? 1 - (j >> 1) : 3 - j], to);
+                    } else {
+                        if (!C::FEW || leader)
+                            load(ma, A_MN, m, p.a_off[0], to);
+                        load(mb, B_MN, n, p.b_off[0], to + C::A_BYTES);
                     }
                     issued |= 1u << stage;
                     issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
@@ -463,36 +468,60 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
                     }
                     tc_fence_after();
                     const uint32_t d = tmem + slot * 256;
-                    for (int kb = kp; kb < ke; ++kb) {
-                        if (!mbar_wait(full_bar(stage), phase, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
+                    // the next stage, once its bytes are there (0: gave up)
+                    auto take = [&](int &st) {
+                        st = stage;
+                        if (!mbar_wait(full_bar(stage), phase, abort_flag))
+                            return false;
                         tc_fence_after();
-                        const uint32_t sA = base + stage * C::STAGE_BYTES;
-                        const uint32_t sB = sA + (SPLIT ? SPLIT : 1) * C::A_BYTES;
-                        constexpr int PRODUCTS = SPLIT ? 3 : 1;
-#pragma unroll
-                        for (int kk = 0; kk < GEMM_BK / 16; ++kk) {
-#pragma unroll
-                            for (int j = 0; j < PRODUCTS; ++j) {
-                                // the smallest product of parts first
-                                const int ai = SPLIT == 3 ? 2 - j : SPLIT == 2 ? (j == 0 ? 1 : 0) : 0;
-                                const int bi = SPLIT == 2 ? (j == 1 ? 1 : 0) : 0;
-                                const uint32_t a = sA + ai * C::A_BYTES, b = sB + bi * PG_B_BYTES;
-                                // 16 K: 32 B along a K-major row, 2048 B (two 8-row atoms) of an MN-major operand
-                                umma_bf16_pair(d,
-                                               A_MN ? sdesc_mnmajor_sw128(a + kk * 2048, PG_ATOM)
-                                                    : sdesc_kmajor_sw128(a + kk * 32),
-                                               B_MN ? sdesc_mnmajor_sw128(b + kk * 2048, PG_ATOM)
-                                                    : sdesc_kmajor_sw128(b + kk * 32),
-                                               IDESC, (kb > kp || kk > 0 || j > 0) ? 1u : 0u);
-                            }
-                        }
-                        umma_commit_pair(empty_bar(stage), 0x3);      // both CTAs' stage is read
                         if (++stage == C::STAGES) {
                             stage = 0;
                             phase ^= 1u;
+                        }
+                        return true;
+                    };
+                    auto multiply = [&](uint32_t a, uint32_t b, bool first) {
+#pragma unroll
+                        for (int kk = 0; kk < GEMM_BK / 16; ++kk)
+                            // 16 K: 32 B along a K-major row, 2048 B (two 8-row atoms) of an MN-major operand
+                            umma_bf16_pair(d,
+                                           A_MN ? sdesc_mnmajor_sw128(a + kk * 2048, PG_ATOM)
+                                                : sdesc_kmajor_sw128(a + kk * 32),
+                                           B_MN ? sdesc_mnmajor_sw128(b + kk * 2048, PG_ATOM)
+                                                : sdesc_kmajor_sw128(b + kk * 32),
+                                           IDESC, (!first || kk > 0) ? 1u : 0u);
+                    };
+                    auto at = [&](int st) { return base + st * C::STAGE_BYTES; };
+                    for (int kb = kp; ok && kb < ke; ++kb) {
+                        int s0, s1, s2, s3;
+                        if constexpr (SPLIT == 0) {
+                            if (!(ok = take(s0)))
+                                break;
+                            multiply(at(s0), at(s0) + C::A_BYTES, kb == kp);
+                            umma_commit_pair(empty_bar(s0), 0x3);     // both CTAs' stage is read
+                        } else {
+                            if (!(ok = take(s0) && take(s1)))
+                                break;
+                            if (SPLIT == 2)
+                                multiply(at(s0), at(s1), kb == kp);   // A middle, B high
+                            else
+                                multiply(at(s1), at(s0), kb == kp);   // A low, B
+                            umma_commit_pair(empty_bar(SPLIT == 2 ? s0 : s1), 0x3);
+                            if (!(ok = take(s2)))
+                                break;
+                            if (SPLIT == 2)
+                                multiply(at(s2), at(s1), false);      // A high, B high
+                            else
+                                multiply(at(s2), at(s0), false);      // A middle, B
+                            umma_commit_pair(empty_bar(SPLIT == 2 ? s1 : s2), 0x3);
+                            if (!(ok = take(s3)))
+                                break;
+                            if (SPLIT == 2)
+                                multiply(at(s2), at(s3), false);      // A high, B middle
+                            else
+                                multiply(at(s3), at(s0), false);      // A high, B
+                            umma_commit_pair(empty_bar(SPLIT == 2 ? s2 : s0), 0x3);
+                            umma_commit_pair(empty_bar(s3), 0x3);
                         }
                     }
                     if (ok) {
