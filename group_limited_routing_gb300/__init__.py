@@ -11,15 +11,20 @@ seeded input generators) imports without the CUDA library.
 import importlib
 
 __all__ = ["moe", "workloads", "build", "MoeConfig", "MoELayer", "route", "forward", "router_logits",
-           "route_from_logits", "Workspace"]
+           "route_from_logits", "Workspace", "train", "TrainStack", "VocabHead", "vocab_loss",
+           "vocab_loss_backward", "block_norm", "block_norm_backward", "route_backward"]
 
 _FROM_MOE = {"MoeConfig", "MoELayer", "route", "forward", "router_logits", "route_from_logits", "Workspace",
-             "last_launch_count", "workspace_bytes"}
+             "last_launch_count", "workspace_bytes", "vocab_loss", "vocab_loss_backward", "block_norm",
+             "block_norm_backward", "route_backward"}
+_FROM_TRAIN = {"TrainStack", "VocabHead"}
 
 
 def __getattr__(name):
     if name in _FROM_MOE:
         return getattr(importlib.import_module(".moe", __name__), name)
-    if name in ("moe", "workloads", "build", "_lib"):
+    if name in _FROM_TRAIN:
+        return getattr(importlib.import_module(".train", __name__), name)
+    if name in ("moe", "train", "workloads", "build", "_lib"):
         return importlib.import_module("." + name, __name__)
     raise AttributeError(name)

@@ -45,35 +45,7 @@ NormLayout norm_layout(int T, int H, int groups)
 }
 
 // ------------------------------------------------------------ dense products
-constexpr int PAIRS = 76;     // CTA pairs of a full GB300
-
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
-
-// K splits of a product with few output tiles: the number that finishes
-// soonest when a pair takes units of kblocks / splits K blocks one after the
-// other, each with an epilogue that costs about EPILOGUE_BLOCKS more, and every
-// split's sums (`elements` of them) are written and read once more by a kernel
-// of its own (SUM_BLOCKS).  One K block
-// takes a pair 0.27 us, in which HBM moves 450,000 fp32 values.  The number
-// depends on the shape alone, so results do not change with the device's load.
-constexpr int EPILOGUE_BLOCKS = 4, SUM_BLOCKS = 10;
-constexpr double ELEMENTS_PER_BLOCK = 450e3;
-
-int choose_splits(int tiles, int kblocks, double elements, int max_splits, int min_blocks)
-{
-    int best = 1;
-    double best_cost = 0.0;
-    for (int n = 1; n <= max_splits && (n == 1 || kblocks / n >= min_blocks); ++n) {
-        const double cost = (double)ceil_div((long long)tiles * n, PAIRS) *
-                                (ceil_div(kblocks, n) + EPILOGUE_BLOCKS) +
-                            (n > 1 ? SUM_BLOCKS : 0) + 2.0 * n * elements / ELEMENTS_PER_BLOCK;
-        if (n == 1 || cost < best_cost) {
-            best = n;
-            best_cost = cost;
-        }
-    }
-    return best;
-}
 
 // K blocks per accumulator of the loss's logits (512 of K): the tensor core's
 // own running sum then stays as close to the exact one as an fp32 library
@@ -97,7 +69,7 @@ constexpr size_t VOCAB_PIECE_BYTES = 1ull << 30;
 
 struct VocabLayout {
     size_t meta, row_of, target, packed_of, lse, weight, logit, stats, hidden, dz, part, total;
-    int ntiles, nstats, piece, splits, split_rows;
+    int ntiles, nstats, piece, part_rows;
 };
 
 VocabLayout vocab_layout(int T, int H, int V, bool backward)
@@ -123,9 +95,11 @@ VocabLayout vocab_layout(int T, int H, int V, bool backward)
         const size_t most = std::max<size_t>(1, VOCAB_PIECE_BYTES / (512ull * T));   // 256-column blocks
         L.piece = (int)std::min<size_t>(L.ntiles, most) * 256;
         L.dz = take(2ull * T * L.piece);
-        L.split_rows = ceil_div(T, 256) * 256;
-        L.splits = choose_splits(ceil_div(T, 256) * ceil_div(H, 256), L.piece / GEMM_BK, (double)T * H, 16, 8);
-        L.part = take(4ull * L.splits * L.split_rows * H);
+        // fp32 sums of d_hidden: one slice per split, and as few rows as count
+        // (which the host does not know) may be split the most
+        const int h_tiles = ceil_div(H, 256), m_tiles = ceil_div(T, 256);
+        L.part_rows = 256 * std::max(m_tiles, std::min(VOCAB_MAX_SPLITS * m_tiles, SPLIT_MAX_UNITS / h_tiles));
+        L.part = take(4ull * L.part_rows * H);
     } else {
         L.logit = take(4ull * T);
         L.stats = take(sizeof(float2) * (size_t)L.nstats * T);
@@ -167,7 +141,7 @@ RouteBwdLayout route_bwd_layout(const moe_cfg &c)
     };
     L.split = take(3ull * c.E * c.H * 2);
     L.parts = take(3ull * c.T * c.E * 2);
-    L.splits = choose_splits(ceil_div(c.H, 256), 3 * ceil_div(c.T, GEMM_BK), 256.0 * c.H, 64, 3);
+    L.splits = choose_splits(ceil_div(c.H, 256), 3 * ceil_div(c.T, GEMM_BK), 256ll * c.H, 64, 3);
     L.part = take(L.splits > 1 ? 4ull * L.splits * 256 * c.H : 0);
     L.total = off;
     return L;
@@ -387,6 +361,7 @@ int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hid
     rp.packed = at<uint16_t>(ws, L.hidden);
     rp.H = H;
     rp.packed_of = at<int>(ws, L.packed_of);
+    rp.dx_kblocks = L.piece / GEMM_BK;
     rp.lse = lse;
     rp.d_loss = d_loss;
     rp.packed_lse = at<float>(ws, L.lse);
@@ -416,17 +391,15 @@ int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hid
     // d_hidden partial sums [splits][rows, H] += dz W
     memset(&px, 0, sizeof(px));
     if (!make_map_bf16(&px.tmA, dz, T, L.piece, GEMM_BK, 128) || !make_map_bf16(&px.tmB, W_vocab, V, H, 64, GEMM_BK) ||
-        !make_map_f32(&px.tmOut, part, (uint64_t)L.splits * L.split_rows, H, 32, 32))
+        !make_map_f32(&px.tmOut, part, L.part_rows, H, 32, 32))
         return MOE_ERR_CUDA;
     px.T = T;
     px.meta = meta;
     px.m_from_rows = 1;
     px.N = H;
-    px.splits = L.splits;
     px.group_m = 1;
-    px.out_rows = L.splits * L.split_rows;
+    px.out_rows = L.part_rows;
     px.out_cols = H;
-    px.split_rows = L.split_rows;
     px.status = status;
     // dW piece = dz^T hidden
     memset(&pw, 0, sizeof(pw));
@@ -454,13 +427,12 @@ int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hid
         px.kblocks = px.part_blocks = ceil_div(n, GEMM_BK);
         px.b_off[0] = v0;
         px.accumulate = v0 > 0;
-        GLR_LAUNCH(KID_VOCAB_DX, launch_pair_gemm(PG_PARTIAL, PP_DX, px, m_tiles * h_tiles * L.splits, s));
+        GLR_LAUNCH(KID_VOCAB_DX, launch_pair_gemm(PG_PARTIAL, PP_DX, px, PAIRS, s));
         pw.M = n;
         pw.out_row0 = v0;
         GLR_LAUNCH(KID_VOCAB_DW, launch_pair_gemm(PG_BF16, PP_DW, pw, ceil_div(n, 256) * h_tiles, s));
     }
-    GLR_LAUNCH(KID_VOCAB_DX, launch_vocab_dx_join(part, L.splits, (long long)L.split_rows * H, meta, rp.packed_of, T, H,
-                                                  d_hidden, s));
+    GLR_LAUNCH(KID_VOCAB_DX, launch_vocab_dx_join(part, meta, rp.packed_of, T, H, d_hidden, s));
     set_last_launches(launches);
     return MOE_OK;
 }

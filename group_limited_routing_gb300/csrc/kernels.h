@@ -349,11 +349,45 @@ cudaError_t launch_expert_feedback(const int32_t *counts, int E, int T, int k, f
 enum PairEpilogue { PG_STATS = 0, PG_DLOGITS = 1, PG_PARTIAL = 2, PG_BF16 = 3, PG_BF16_ADD = 4, PG_STATS_FEW = 5 };
 constexpr int PAIR_FEW_ROWS = 32;
 
+// K splits of a product with few output tiles: the number that finishes
+// soonest when a pair takes units of kblocks / splits K blocks one after the
+// other, each with an epilogue that costs about EPILOGUE_BLOCKS more, and every
+// split's sums (`elements` of them) are written and read once more by a kernel
+// of its own (SUM_BLOCKS).  One K block takes a pair 0.27 us, in which HBM moves
+// 450,000 fp32 values.  The number depends on the shape alone, so results do
+// not change with the device's load.
+constexpr int PAIRS = 76;              // CTA pairs of a full GB300
+constexpr int SPLIT_MAX_UNITS = 608;   // tiles times splits, when split at all
+__host__ __device__ inline long long split_cost(int tiles, int kblocks, long long elements, int n)
+{
+    constexpr long long EPILOGUE_BLOCKS = 4, SUM_BLOCKS = 10, ELEMENTS_PER_BLOCK = 450000;
+    const int waves = (int)(((long long)tiles * n + PAIRS - 1) / PAIRS);
+    return waves * ((kblocks + n - 1) / n + EPILOGUE_BLOCKS) + (n > 1 ? SUM_BLOCKS : 0) +
+           2 * n * elements / ELEMENTS_PER_BLOCK;
+}
+
+__host__ __device__ inline bool may_split(int tiles, int kblocks, int n, int min_blocks)
+{
+    return n == 1 || (kblocks / n >= min_blocks && (long long)tiles * n <= SPLIT_MAX_UNITS);
+}
+
+// the cheapest, and of equal ones the fewest
+inline int choose_splits(int tiles, int kblocks, long long elements, int max_splits, int min_blocks)
+{
+    int best = 1;
+    for (int n = 2; n <= max_splits && may_split(tiles, kblocks, n, min_blocks); ++n)
+        if (split_cost(tiles, kblocks, elements, n) < split_cost(tiles, kblocks, elements, best))
+            best = n;
+    return best;
+}
+
 // What the vocabulary operators' row kernel leaves for the kernels after it.
 struct VocabMeta {
     int rows;      // rows that count (target in [0, V) and not ignored)
     float scale;   // backward: largest |d_loss| of them (1 when that is not finite)
+    int splits;    // backward: K splits of the d_hidden product over those rows
 };
+constexpr int VOCAB_MAX_SPLITS = 16, VOCAB_MIN_SPLIT_BLOCKS = 8;
 
 struct PairGemmParams {
     CUtensorMap tmA, tmB, tmOut;
@@ -367,12 +401,12 @@ struct PairGemmParams {
     int M, N;
     int kblocks;              // K in blocks of 64
     int a_off[3], b_off[2];   // rows added to the operand's row coordinate (of each part)
-    int splits;               // K range cut among this many units
+    int splits;               // K range cut among this many units; 0: meta->splits
     int part_blocks;          // K blocks per accumulator (STATS, PARTIAL; else at least kblocks)
     int group_m;              // tiles run m-fastest within groups of this many m-tiles
     int out_row0;             // row of the output map where row 0 goes
     int out_rows, out_cols;   // the output map's extent
-    int split_rows;           // PG_PARTIAL: rows between the splits' slices
+    int split_rows;           // PG_PARTIAL: rows between the splits' slices; 0: M rounded up to 256
     int accumulate;           // PG_PARTIAL: add to the slice
     // PG_STATS, PG_DLOGITS
     const int *target;        // per packed row
@@ -403,6 +437,7 @@ struct VocabRowsParams {
     const uint16_t *hidden;   // [T, H]
     uint16_t *packed;         // the counting rows' copies where some row does not count
     int H;
+    int dx_kblocks;           // backward: K blocks of the d_hidden product (of a vocabulary piece)
     float *loss, *lse_out;    // forward: zeroed where a row does not count
     // backward
     int *packed_of;           // row -> packed row, or -1
@@ -413,8 +448,8 @@ cudaError_t launch_vocab_rows(const VocabRowsParams &p, cudaStream_t s);
 cudaError_t launch_vocab_join(const float2 *stats, int ntiles, int ld, const float *target_logit,
                               const VocabMeta *meta, const int *row_of, int T, float *loss, float *lse,
                               cudaStream_t s);
-cudaError_t launch_vocab_dx_join(const float *part, int splits, long long split_stride, const VocabMeta *meta,
-                                 const int *packed_of, int T, int H, uint16_t *d_hidden, cudaStream_t s);
+cudaError_t launch_vocab_dx_join(const float *part, const VocabMeta *meta, const int *packed_of, int T, int H,
+                                 uint16_t *d_hidden, cudaStream_t s);
 
 // ---- the router's gradient (route_grad.cu) --------------------------------------
 // (logits: nparts buffers of [T, E], one after the other, to be added)

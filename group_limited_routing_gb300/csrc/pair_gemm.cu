@@ -101,7 +101,7 @@ struct Unit {
 };
 
 struct Shape {
-    int M, m_tiles, n_tiles, kblocks, units;
+    int M, m_tiles, n_tiles, kblocks, splits, split_rows, units;
 };
 
 __device__ __forceinline__ Shape shape_of(const PairGemmParams &p)
@@ -112,7 +112,9 @@ __device__ __forceinline__ Shape shape_of(const PairGemmParams &p)
     sh.kblocks = p.k_from_rows ? (rows + GEMM_BK - 1) / GEMM_BK : p.kblocks;
     sh.m_tiles = (sh.M + PG_BM - 1) / PG_BM;
     sh.n_tiles = (p.N + PG_BN - 1) / PG_BN;
-    sh.units = sh.m_tiles * sh.n_tiles * p.splits;
+    sh.splits = p.splits ? p.splits : p.meta->splits;
+    sh.split_rows = p.split_rows ? p.split_rows : sh.m_tiles * PG_BM;
+    sh.units = sh.m_tiles * sh.n_tiles * sh.splits;
     return sh;
 }
 
@@ -128,8 +130,8 @@ __device__ __forceinline__ Unit unit_of(const PairGemmParams &p, const Shape &sh
     t.nt = in / gm;
     t.m0 = (g * p.group_m + in % gm) * PG_BM;
     t.n0 = t.nt * PG_BN;
-    t.k0 = (int)((long long)sh.kblocks * t.split / p.splits);
-    t.k1 = (int)((long long)sh.kblocks * (t.split + 1) / p.splits);
+    t.k0 = (int)((long long)sh.kblocks * t.split / sh.splits);
+    t.k1 = (int)((long long)sh.kblocks * (t.split + 1) / sh.splits);
     t.parts = (t.k1 - t.k0 + p.part_blocks - 1) / p.part_blocks;
     return t;
 }
@@ -276,10 +278,10 @@ __device__ __forceinline__ void epilogue_dlogits(const PairGemmParams &p, const 
 
 // The warp's fp32 sums into the split's slice.  Each element is stored or added
 // to once per launch, so the sums' order is that of the launches.
-__device__ __forceinline__ void epilogue_partial(const PairGemmParams &p, const Unit &t, const uint32_t (&z)[PG_HALF],
-                                                 int half, int row0, int lane, uint8_t *box)
+__device__ __forceinline__ void epilogue_partial(const PairGemmParams &p, const Shape &sh, const Unit &t,
+                                                 const uint32_t (&z)[PG_HALF], int half, int row0, int lane, uint8_t *box)
 {
-    const int row = t.split * p.split_rows + row0;
+    const int row = t.split * sh.split_rows + row0;
 #pragma unroll
     for (int c = 0; c < PG_HALF; c += 32) {
         const int col = t.n0 + half * PG_HALF + c;
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
                     if (row0 < sh.M)
                         epilogue_stats(p, sh, t, z, half, row0 + lane);
                 } else
-                    epilogue_partial(p, t, z, half, row0, lane, boxes);
+                    epilogue_partial(p, sh, t, z, half, row0, lane, boxes);
             } else {
                 // (one part: the accumulator's values are used as they are)
                 const bool empty = t.parts == 0;

@@ -3,7 +3,10 @@
 // of pair_gemm.cu read.
 //
 // With s = sigmoid(L), S the chosen experts of a token and D = sum_S s + eps,
-// w_j = rsf s_j / D, so  ds_j = rsf / D (dw_j - sum_i dw_i s_i / D).  The balance
+// w_j = rsf s_j / D, so  ds_j = rsf / D (dw_j - sum_i dw_i s_i / D)
+//                            = rsf / D^2 (sum_i (dw_j - dw_i) s_i + dw_j eps),
+// the second form without the first's cancellation (equal dw, or a single
+// expert, leave eps alone).  The balance
 // loss E sum_e f_e mean_t(s_te / Z_t), Z_t = sum_e s_te, f_e = counts_e / (k T)
 // fixed, adds  ds_e += d_aux E / T (f_e - sum_e' f_e' s_e' / Z) / Z.  Then
 // dL = ds s (1 - s), with 1 - s formed as exp(-L) s where L > 0, which keeps its
@@ -111,8 +114,11 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const float *__restrict
         __syncwarp();
         const float sj = e >= 0 ? mine[e] : 0.0f;
         const float D = warp_sum(sj) + eps;
-        const float m = __fdividef(warp_sum(dw * sj), D);
-        float dsj = __fdividef(rsf, D) * (dw - m);
+        float dsj = dw * eps;
+        for (int i = 0; i < k; ++i)
+            dsj = fmaf(dw - __shfl_sync(0xffffffffu, dw, i), __shfl_sync(0xffffffffu, sj, i), dsj);
+        const float per_d = __fdividef(1.0f, D);
+        dsj = dsj * per_d * (rsf * per_d);
         // (an id that a token names more than once, never the router's, adds up
         // in the first lane that names it)
         const unsigned same = __match_any_sync(0xffffffffu, e);

@@ -88,6 +88,18 @@ __global__ void __launch_bounds__(ROWS_THREADS) vocab_rows_kernel(const VocabRow
             p.meta->rows = total;
             p.meta->scale = scale;
         }
+        if (p.packed_of && w == 0) {
+            // choose_splits, a candidate per lane
+            const int n = lane + 1, tiles = (total + 255) / 256 * ((p.H + 255) / 256);
+            const bool may = n <= VOCAB_MAX_SPLITS && may_split(tiles, p.dx_kblocks, n, VOCAB_MIN_SPLIT_BLOCKS);
+            long long key = may ? split_cost(tiles, p.dx_kblocks, (long long)total * p.H, n) * 64 + n
+                                : 0x7fffffffffffffffll;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                key = min(key, __shfl_xor_sync(0xffffffffu, key, off));
+            if (lane == 0)
+                p.meta->splits = (int)(key & 63);
+        }
         int q = r;
 #pragma unroll 4
         for (int t = t0; t < t1; ++t) {
@@ -190,12 +202,13 @@ __global__ void __launch_bounds__(1024) vocab_join_kernel(const float2 *__restri
 
 // d_hidden[t] = bf16( scale sum_s part[s][packed row of t] ), zero where the
 // row does not count.  Splits in order.
-__global__ void __launch_bounds__(128) vocab_dx_join_kernel(const float *__restrict__ part, int splits,
-                                                            long long split_stride, const VocabMeta *meta,
+__global__ void __launch_bounds__(128) vocab_dx_join_kernel(const float *__restrict__ part, const VocabMeta *meta,
                                                             const int *packed_of, int T, int H, uint16_t *d_hidden)
 {
     pdl_wait();
     const float scale = meta->scale;
+    const int splits = meta->splits;
+    const size_t split_stride = (size_t)((meta->rows + 255) / 256 * 256) * H;
     const int nv = H / 8;
     for (int t = blockIdx.x; t < T; t += gridDim.x) {
         const int r = packed_of[t];
@@ -241,12 +254,12 @@ cudaError_t launch_vocab_join(const float2 *stats, int nstats, int ld, const flo
     return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
 
-cudaError_t launch_vocab_dx_join(const float *part, int splits, long long split_stride, const VocabMeta *meta,
-                                 const int *packed_of, int T, int H, uint16_t *d_hidden, cudaStream_t s)
+cudaError_t launch_vocab_dx_join(const float *part, const VocabMeta *meta, const int *packed_of, int T, int H,
+                                 uint16_t *d_hidden, cudaStream_t s)
 {
     const int blocks = T < 2432 ? T : 2432;
-    const cudaError_t e = launch_pdl(vocab_dx_join_kernel, dim3(blocks), dim3(128), 0, s, part, splits, split_stride,
-                                     meta, packed_of, T, H, d_hidden);
+    const cudaError_t e = launch_pdl(vocab_dx_join_kernel, dim3(blocks), dim3(128), 0, s, part, meta,
+                                     packed_of, T, H, d_hidden);
     return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
 

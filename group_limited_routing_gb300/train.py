@@ -1,0 +1,127 @@
+"""A training step of a stack of MoE layers: the norms around every block, the
+layers, the loss over the vocabulary, and the gradients of all of them.
+
+    step = TrainStack(layers, VocabHead(W_vocab, T), w_pre, w_post, gate)
+    loss, lse = step(x, target)                # x [T, H]: the residual stream
+    grads = step.backward(d_loss)              # d_loss [T]: 1 / n for the mean over n rows
+
+Layer l of L computes, with n_0 = RMS(x) w_pre[0],
+    y_l = layer_l(n_l)
+    r_{l+1}, n_{l+1} = block_norm(r_l, y_l, gate[l], w_post[l], w_pre[l + 1])
+and the head's loss is that of n_L.  Everything runs in the library's kernels
+on the current stream; this module only passes tensors between them.
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import moe
+
+
+class VocabHead:
+    """The vocabulary's weight [V, H] bf16 and the workspaces of its loss:
+    __call__(hidden, target) is vocab_loss, backward(d_loss) the gradient of the
+    last call."""
+
+    def __init__(self, W_vocab, T: int, ignore_index: int = -100):
+        V, H = W_vocab.shape
+        self.W_vocab, self.ignore_index = W_vocab, ignore_index
+        self.device = W_vocab.device
+        self.ws = moe.vocab_loss_workspace(T, H, V, device=self.device)
+        self.ws_bwd = None
+        self._shape = (T, H, V)
+        self._last = None
+
+    def __call__(self, hidden, target):
+        loss, lse = moe.vocab_loss(hidden, self.W_vocab, target, ignore_index=self.ignore_index, ws=self.ws)
+        self._last = (hidden, target, lse)
+        return loss, lse
+
+    def backward(self, d_loss, out: Optional[dict] = None) -> dict:
+        """dict(d_hidden [T, H] bf16, dW_vocab [V, H] bf16)."""
+        if self._last is None:
+            raise RuntimeError("backward() needs a forward call first")
+        if self.ws_bwd is None:
+            self.ws_bwd = moe.vocab_loss_workspace(*self._shape, backward=True, device=self.device)
+        hidden, target, lse = self._last
+        return moe.vocab_loss_backward(hidden, self.W_vocab, target, lse, d_loss, ignore_index=self.ignore_index,
+                                       ws=self.ws_bwd, out=out)
+
+    def status(self) -> int:
+        return self.ws.status() | (self.ws_bwd.status() if self.ws_bwd is not None else 0)
+
+
+class TrainStack:
+    """layers: MoELayer objects of one configuration (aux=True adds the balance
+    loss); w_pre [L + 1, H], w_post [L, H] and gate [L, H] or [L, groups, H] fp32;
+    alpha the residual scale."""
+
+    def __init__(self, layers, head: VocabHead, w_pre, w_post, gate, alpha: float = 1.0, eps: float = 1e-6):
+        self.layers = list(layers)
+        self.head = head
+        self.w_pre, self.w_post = w_pre, w_post
+        self.gate = gate if gate.dim() == 3 else gate[:, None, :]
+        self.alpha, self.eps = alpha, eps
+        self.cfg = self.layers[0].cfg
+        self.device = self.layers[0].device
+        self.ws_route = moe.route_backward_workspace(self.cfg, self.device)
+        self.ws_norm = moe.block_norm_workspace(self.cfg.T, self.cfg.H, self.gate.shape[1], self.device)
+        self._saved = None
+
+    def __call__(self, x, target):
+        """(loss [T], lse [T]) of the stack on the residual stream x [T, H] (bf16
+        or fp32)."""
+        r, n = moe.block_norm(x, w_pre=self.w_pre[0], eps=self.eps)
+        saved = []
+        for i, layer in enumerate(self.layers):
+            y = layer(n)
+            saved.append((r, y))
+            r, n = moe.block_norm(r, y, self.gate[i], self.w_post[i], self.w_pre[i + 1], alpha=self.alpha,
+                                  eps=self.eps)
+        self._saved = (x, saved)
+        return self.head(n, target)
+
+    def aux_loss(self):
+        """The last call's balance losses, one per layer ([1] fp32 each)."""
+        return [layer.routing[4] for layer in self.layers]
+
+    def backward(self, d_loss, d_aux_loss=None) -> dict:
+        """Gradients of the last call for d_loss [T] fp32 (and d_aux_loss [1] fp32,
+        the weight of every layer's balance loss): dict(d_x, dW_vocab, dw_pre
+        [L + 1, H], dw_post [L, H], d_gate [L, groups, H], layers: per layer what
+        moe.backward gives with d_hidden replaced by the whole one, and dW_router)."""
+        if self._saved is None:
+            raise RuntimeError("backward() needs a forward call first")
+        x, saved = self._saved
+        head = self.head.backward(d_loss)
+        d_n, d_r = head["d_hidden"], None
+        out = dict(dW_vocab=head["dW_vocab"], dw_pre=torch.empty_like(self.w_pre), dw_post=torch.empty_like(self.w_post),
+                   d_gate=torch.empty_like(self.gate), layers=[None] * len(self.layers))
+        for i in reversed(range(len(self.layers))):
+            r, y = saved[i]
+            g = moe.block_norm_backward(r, y, self.gate[i], self.w_post[i], self.w_pre[i + 1], d_r, d_n,
+                                        alpha=self.alpha, eps=self.eps, ws=self.ws_norm,
+                                        out=dict(dw_pre=out["dw_pre"][i + 1], dw_post=out["dw_post"][i],
+                                                 d_gate=out["d_gate"][i], d_y=d_n, **({} if d_r is None else {"d_x": d_r})))
+            d_r = g["d_x"]
+            layer = self.layers[i]
+            e = layer.backward(g["d_y"])
+            rb = moe.route_backward(self.cfg, layer._hidden, layer.W_router, layer.routing[0], e["d_topk_w"],
+                                    d_aux_loss=d_aux_loss, expert_counts=None if d_aux_loss is None else layer.routing[2],
+                                    d_hidden_add=e["d_hidden"], W_split=layer.W_split, ws=self.ws_route,
+                                    out=dict(d_hidden=e["d_hidden"]))
+            e["dW_router"] = rb["dW_router"]
+            out["layers"][i] = e
+            d_n = rb["d_hidden"]
+        g = moe.block_norm_backward(x, None, None, None, self.w_pre[0], d_r, d_n, eps=self.eps, ws=self.ws_norm,
+                                    out=dict(dw_pre=out["dw_pre"][0]))
+        out["d_x"] = g["d_x"]
+        return out
+
+    def status(self) -> int:
+        st = self.head.status() | self.ws_route.status()
+        for layer in self.layers:
+            st |= layer.status()
+        return st
