@@ -709,6 +709,63 @@ def report(args, world, w0, ms_max, prof, nprof, e2e_ms, launches, clk, extra):
     return line
 
 
+def run_train(args, rank, local):
+    """The training step (train.TrainStack): forward and every gradient of
+    --train-layers MoE layers with their norms, and of the loss over --vocab
+    words, inputs resident.  One JSON line of its own metric, with the kernels'
+    shares."""
+    from group_limited_routing_gb300 import moe, train, workloads as wl
+
+    dev = torch.device("cuda", local)
+    torch.cuda.set_device(dev)
+    w0 = wl.WORKLOADS[5].with_T(args.tokens or 8192)
+    T, H = w0.T, w0.H
+    cfg = moe.MoeConfig(T=T, H=H, I=w0.I, Is=w0.Is)
+    layers = []
+    for i in range(args.train_layers):
+        d = wl.layer_inputs(w0, dev, layer=i)
+        layers.append(moe.MoELayer(cfg, d["W_router"], d["expert_bias"], d["W_gate_up"], d["W_down"],
+                                   d["shared_gate_up"], d["shared_down"], aux=True))
+    g = torch.Generator(device=dev)
+    g.manual_seed(7)
+    head = train.VocabHead((torch.randn(args.vocab, H, generator=g, device=dev) * 0.02).to(torch.bfloat16), T)
+    ones = lambda *s: torch.ones(*s, device=dev)  # noqa: E731
+    L = len(layers)
+    step = train.TrainStack(layers, head, ones(L + 1, H), ones(L, H), ones(L, H))
+    x = wl.hidden(w0, dev, layer=rank)
+    target = torch.randint(0, args.vocab, (T,), generator=g, device=dev)
+    d_loss = torch.full((T,), 1.0 / T, device=dev)
+    d_aux = torch.full((1,), 1e-2, device=dev)
+
+    def once():
+        step(x, target)
+        step.backward(d_loss, d_aux)
+
+    for _ in range(args.warmup):
+        once()
+    torch.cuda.synchronize(dev)
+    if step.status() != 0:
+        raise RuntimeError("device status after warm-up: %d" % step.status())
+    e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    e0.record()
+    for _ in range(args.steps):
+        once()
+    e1.record()
+    torch.cuda.synchronize(dev)
+    ms = e0.elapsed_time(e1) / args.steps
+    moe.profile_enable(True)
+    moe.profile_read()
+    once()
+    torch.cuda.synchronize(dev)
+    prof = moe.profile_read()
+    moe.profile_enable(False)
+    return {"metric": "training step (forward + all gradients), tokens/s", "value": T / ms * 1e3, "unit": "tokens/s",
+            "n_gpus": 1, "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms, "higher_is_better": True,
+            "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+            "config": {"model": "%d MoE layers with norms, vocabulary %d" % (L, args.vocab), "global_batch": T, "H": H},
+            "kernels_ms": {k: round(v[0], 4) for k, v in prof.items() if v[1]}}
+
+
 def run_reference(args, world, rank):
     """The CPU oracle as it stands, on the host cores, one bounded sample per step."""
     if rank != 0:
@@ -761,6 +818,11 @@ def main():
     ap.add_argument("--no-graph", action="store_true", help="skip the CUDA-graph replay timing")
     ap.add_argument("--backward", action="store_true",
                     help="time the layer's backward (moe_backward, routing fixed) instead of its forward")
+    ap.add_argument("--train", action="store_true",
+                    help="time a training step: norms, layers, vocabulary loss and all their gradients (a line of its "
+                         "own metric)")
+    ap.add_argument("--train-layers", type=int, default=2, help="MoE layers of the training step")
+    ap.add_argument("--vocab", type=int, default=32768, help="vocabulary of the training step's loss")
     ap.add_argument("--dense", type=int, default=0, metavar="I",
                     help="time the dense first-layer MLP of intermediate size I instead of the MoE layer")
     ap.add_argument("--flush-l2", action="store_true",
@@ -788,7 +850,7 @@ def main():
         line = run_reference(args, world, rank)
     else:
         world, rank, local = init_dist()
-        line = run_ours(args, world, rank, local)
+        line = run_train(args, rank, local) if args.train else run_ours(args, world, rank, local)
         if world > 1:
             import torch.distributed as dist
             dist.destroy_process_group()

@@ -51,8 +51,9 @@ template <int EPI>
 constexpr bool IS_STATS = EPI == PG_STATS || EPI == PG_STATS_FEW;
 
 // Shared memory: a ring of operand stages, and per epilogue warp the 4 KB
-// boxes its output leaves through (none for the statistics; two for bf16
-// outputs, whose addend arrives in the same boxes ahead of the accumulator).
+// box its output leaves through (none for the statistics; two where an addend
+// arrives in them ahead of the accumulator).  A sixth stage is worth more than a
+// second box: with five, the long products of the loss's gradient took 3% more.
 // PG_STATS_FEW is for at most PAIR_FEW_ROWS rows, where the product streams B
 // from memory: a stage holds those rows of A only, and the shared memory this
 // frees goes to a deeper ring of B.  The MMA still reads 128 rows per CTA; the
@@ -70,7 +71,7 @@ struct PgCfg {
     static constexpr int A_ROWS = FEW ? PAIR_FEW_ROWS : 128;
     static constexpr int A_BYTES = A_ROWS * GEMM_BK * 2;
     static constexpr int STAGE_BYTES = SPLIT ? PG_B_BYTES : A_BYTES + PG_B_BYTES;
-    static constexpr int BUFS = IS_STATS<EPI> ? 0 : EPI == PG_BF16 || EPI == PG_BF16_ADD ? 2 : 1;
+    static constexpr int BUFS = IS_STATS<EPI> ? 0 : EPI == PG_BF16_ADD ? 2 : 1;
     static constexpr int STAGING = BUFS * PG_EPI_WARPS * 4096;
     static constexpr int STAGES = (230400 - STAGING) / STAGE_BYTES;
     static constexpr int NBARS = 2 * STAGES + 2 * PG_SLOTS + 1 + PG_EPI_WARPS;
@@ -652,10 +653,9 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
                     bf16_box<false>(tacc() + 64, empty, scale, nullptr, lane, v[1]);
                     if (!empty)
                         release();
-                    if (lane == 0)
-                        bulk_wait_group_read<0>();      // the tile before has left the boxes
-                    __syncwarp();
-                    store_boxes(p, boxes, v, lane, col0, row0 + p.out_row0);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        store_box<false>(p, boxes, v[i], lane, col0 + 64 * i, row0 + p.out_row0);
                 } else {
                     epilogue_dlogits(p, sh, t, tacc() - half * PG_HALF, half, row0 + lane, row0, lane, boxes);
                     release();

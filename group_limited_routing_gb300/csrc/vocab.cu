@@ -27,72 +27,75 @@ constexpr int ROWS_THREADS = 1024;
 
 }  // namespace
 
-// Which rows count, and their packed order: thread i counts the rows of its
-// run of rows, a scan over the threads gives each its first packed row.  Every
-// block does this for all rows (a few loads per thread, and no block waits for
-// another); block 0 writes the results, and all of them, where some row does
-// not count, copy the counting rows' hidden states side by side and then zero
-// rows up to a multiple of 64 (a K block of the weight gradient).  Where every
-// row counts the products read `hidden` itself.
+// Which rows count, and their packed order.  Block b owns rows [b T / grid,
+// (b + 1) T / grid).  It counts those before them and all of them (every block
+// reads every target: a few coalesced loads per thread, and no block waits for
+// another), packs its own rows behind the ones before, and, where some row of
+// the batch does not count, copies its rows' hidden states side by side.  Rows
+// of zeros follow up to a multiple of 64 (a K block of the weight gradient).
+// Where every row counts the products read `hidden` itself.
 __global__ void __launch_bounds__(ROWS_THREADS) vocab_rows_kernel(const VocabRowsParams p)
 {
-    __shared__ int warp_sum[32];
-    __shared__ float warp_max[32];
+    __shared__ int sums[32], befores[32], own[32];
+    __shared__ float tops[32];
+    __shared__ int list[ROWS_THREADS];
     pdl_wait();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const bool writer = blockIdx.x == 0;
-    const int per = (p.T + ROWS_THREADS - 1) / ROWS_THREADS;
-    const int t0 = min(p.T, (int)threadIdx.x * per), t1 = min(p.T, t0 + per);
-    int n = 0;
+    const int blocks = gridDim.x;
+    const int t0 = (int)((long long)blockIdx.x * p.T / blocks), t1 = (int)((long long)(blockIdx.x + 1) * p.T / blocks);
+    auto counts = [&](long long v) { return v != p.ignore && v >= 0 && v < p.V; };
+    int n = 0, before = 0;
     bool bad = false;
     float top = 0.0f;
-#pragma unroll 4
-    for (int t = t0; t < t1; ++t) {
+#pragma unroll 8
+    for (int t = threadIdx.x; t < p.T; t += ROWS_THREADS) {
         const long long v = target_at(p, t);
-        const bool counts = v != p.ignore && v >= 0 && v < p.V;
-        bad |= !counts && v != p.ignore;
-        n += counts;
-        if (p.d_loss && writer && counts) {
-            const float g = fabsf(p.d_loss[t]);
-            top = g > top || g != g ? g : top;      // a NaN stays
-        }
+        const bool c = counts(v);
+        const float g = p.d_loss ? fabsf(p.d_loss[t]) : 0.0f;
+        bad |= !c && v != p.ignore;
+        n += c;
+        before += c && t < t0;
+        if (c)
+            top = g > top || g != g ? g : top;          // a NaN stays
     }
-    if (bad && writer)
+    if (bad && blockIdx.x == 0)
         atomicOr(p.status, ST_BAD_TARGET);
-    int at = n;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, at, off);
-        if (lane >= off)
-            at += o;
+    for (int off = 16; off > 0; off >>= 1) {
+        n += __shfl_xor_sync(0xffffffffu, n, off);
+        before += __shfl_xor_sync(0xffffffffu, before, off);
         const float f = __shfl_xor_sync(0xffffffffu, top, off);
         top = f > top || f != f ? f : top;
     }
-    if (lane == 31)
-        warp_sum[w] = at;
-    if (lane == 0)
-        warp_max[w] = top;
-    __syncthreads();
-    int before = 0, total = 0;
-    top = 0.0f;
-    for (int i = 0; i < 32; ++i) {
-        if (i < w)
-            before += warp_sum[i];
-        total += warp_sum[i];
-        top = warp_max[i] > top || warp_max[i] != warp_max[i] ? warp_max[i] : top;
+    if (lane == 0) {
+        sums[w] = n;
+        befores[w] = before;
+        tops[w] = top;
     }
-    int r = before + at - n;
-    if (writer) {
-        const float scale = top > 0.0f && top < INFINITY ? top : 1.0f;
-        if (threadIdx.x == 0) {
+    __syncthreads();
+    // (each warp for itself: lane i takes warp i's sums)
+    n = sums[lane];
+    before = befores[lane];
+    top = tops[lane];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        n += __shfl_xor_sync(0xffffffffu, n, off);
+        before += __shfl_xor_sync(0xffffffffu, before, off);
+        const float f = __shfl_xor_sync(0xffffffffu, top, off);
+        top = f > top || f != f ? f : top;
+    }
+    const int total = n;
+    const float scale = top > 0.0f && top < INFINITY ? top : 1.0f;
+    if (blockIdx.x == 0 && w == 0) {
+        if (lane == 0) {
             p.meta->rows = total;
             p.meta->scale = scale;
         }
-        if (p.packed_of && w == 0) {
+        if (p.packed_of) {
             // choose_splits, a candidate per lane
-            const int n = lane + 1, tiles = (total + 255) / 256 * ((p.H + 255) / 256);
-            const bool may = n <= VOCAB_MAX_SPLITS && may_split(tiles, p.dx_kblocks, n, VOCAB_MIN_SPLIT_BLOCKS);
-            long long key = may ? split_cost(tiles, p.dx_kblocks, (long long)total * p.H, n) * 64 + n
+            const int c = lane + 1, tiles = (total + 255) / 256 * ((p.H + 255) / 256);
+            const bool may = c <= VOCAB_MAX_SPLITS && may_split(tiles, p.dx_kblocks, c, VOCAB_MIN_SPLIT_BLOCKS);
+            long long key = may ? split_cost(tiles, p.dx_kblocks, (long long)total * p.H, c) * 64 + c
                                 : 0x7fffffffffffffffll;
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1)
@@ -100,57 +103,65 @@ __global__ void __launch_bounds__(ROWS_THREADS) vocab_rows_kernel(const VocabRow
             if (lane == 0)
                 p.meta->splits = (int)(key & 63);
         }
-        int q = r;
-#pragma unroll 4
-        for (int t = t0; t < t1; ++t) {
-            const long long v = target_at(p, t);
-            const bool counts = v != p.ignore && v >= 0 && v < p.V;
-            if (p.packed_of)
-                p.packed_of[t] = counts ? q : -1;
-            if (counts) {
-                p.row_of[q] = t;
-                p.packed_target[q] = (int)v;
-                if (p.d_loss) {
-                    p.packed_lse[q] = p.lse[t];
-                    p.packed_weight[q] = p.d_loss[t] / scale;
-                }
-                ++q;
-            } else if (p.loss) {
-                p.loss[t] = 0.0f;
-                p.lse_out[t] = 0.0f;
-            }
-        }
     }
-    if (total == p.T)
-        return;
-    // Block b copies the packed rows congruent to b: each thread meets its own
-    // run's rows again, a warp copies one row at a time.
-    const int nv = p.H / 8, blocks = gridDim.x;
+    const int nv = p.H / 8;
     const uint4 *src = reinterpret_cast<const uint4 *>(p.hidden);
     uint4 *dst = reinterpret_cast<uint4 *>(p.packed);
-    for (int i = 0; i < per; ++i) {
-        const int t = t0 + i;
-        bool mine = false;
-        int q = 0;
-        if (t < t1) {
-            const long long v = target_at(p, t);
-            if (v != p.ignore && v >= 0 && v < p.V) {
-                q = r++;
-                mine = q % blocks == (int)blockIdx.x;
+    for (int first = t0; first < t1; first += ROWS_THREADS) {
+        const int t = first + threadIdx.x;
+        const long long v = t < t1 ? target_at(p, t) : p.ignore;
+        const bool c = t < t1 && counts(v);
+        const unsigned mask = __ballot_sync(0xffffffffu, c);
+        __syncthreads();                                 // (the pass before has read own and list)
+        if (lane == 0)
+            own[w] = __popc(mask);
+        __syncthreads();
+        int mine = own[lane];                            // the warps' sums: inclusive scan over the lanes
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, mine, off);
+            if (lane >= off)
+                mine += o;
+        }
+        const int here = __shfl_sync(0xffffffffu, mine, 31);
+        const int rank = (w ? __shfl_sync(0xffffffffu, mine, w - 1) : 0) + __popc(mask & ((1u << lane) - 1u));
+        const int q = before + rank;
+        if (t < t1 && p.packed_of)
+            p.packed_of[t] = c ? q : -1;
+        if (c) {
+            list[rank] = t;
+            p.row_of[q] = t;
+            p.packed_target[q] = (int)v;
+            if (p.d_loss) {
+                p.packed_lse[q] = p.lse[t];
+                p.packed_weight[q] = p.d_loss[t] / scale;
             }
+        } else if (t < t1 && p.loss) {
+            p.loss[t] = 0.0f;
+            p.lse_out[t] = 0.0f;
         }
-        for (unsigned todo = __ballot_sync(0xffffffffu, mine); todo; todo &= todo - 1) {
-            const int l = __ffs(todo) - 1;
-            const size_t from = (size_t)__shfl_sync(0xffffffffu, t, l) * nv;
-            const size_t to = (size_t)__shfl_sync(0xffffffffu, q, l) * nv;
-#pragma unroll 8
-            for (int v = lane; v < nv; v += 32)
-                dst[to + v] = src[from + v];
-        }
+        __syncthreads();
+        if (total < p.T)
+            for (int i = w; i < here; i += 32) {
+                const size_t from = (size_t)list[i] * nv, to = (size_t)(before + i) * nv;
+                for (int v0 = lane; v0 < nv; v0 += 8 * 32) {
+                    uint4 q8[8];                         // (loads before stores: the compiler may not assume it)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (v0 + 32 * j < nv)
+                            q8[j] = __ldcs(src + from + v0 + 32 * j);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (v0 + 32 * j < nv)
+                            dst[to + v0 + 32 * j] = q8[j];
+                }
+            }
+        before += here;
     }
-    for (int q = total + blockIdx.x; q < min(p.T, (total + 63) / 64 * 64); q += blocks)
-        for (int v = threadIdx.x; v < nv; v += ROWS_THREADS)
-            dst[(size_t)q * nv + v] = make_uint4(0, 0, 0, 0);
+    if (total < p.T)
+        for (int q = total + blockIdx.x; q < min(p.T, (total + 63) / 64 * 64); q += blocks)
+            for (int v = threadIdx.x; v < nv; v += ROWS_THREADS)
+                dst[(size_t)q * nv + v] = make_uint4(0, 0, 0, 0);
 }
 
 // Joins the 128-column blocks' softmax statistics of each row.  A block takes R
