@@ -725,17 +725,26 @@ __global__ void __launch_bounds__(1024) block_norm_finish_kernel(const BlockNorm
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
     const int out = blockIdx.x * 32 + lane;       // warp 0's column
     const bool mine = w == 0 && out < p.H;
-    const float pre = across(in ? some(p.part_b, 0, blocks, slice, 128) : zero);
+    constexpr int FEW = 4;
+    const bool few = p.part_a && p.groups <= FEW;  // a few long groups: the whole block takes each
+    float4 part[1 + FEW];
+    part[0] = in ? some(p.part_b, 0, blocks, slice, 128) : zero;
+#pragma unroll
+    for (int g = 0; g < FEW; ++g)
+        part[1 + g] = in && few && g < p.groups ? some(p.part_a, (size_t)g * p.cpg, p.cpg, slice, 128) : zero;
+    const float pre = across(part[0]);
     if (mine && p.dw_pre)
         p.dw_pre[out] = pre;
     if (!p.part_a)
         return;
-    if (p.groups <= 4) {
-        // a few long groups: one after the other, by the whole block
+    if (few) {
         const float wp = mine && p.w_post ? p.w_post[out] : 1.0f;
         float post = 0.0f;
-        for (int g = 0; g < p.groups; ++g) {
-            const float a = across(in ? some(p.part_a, (size_t)g * p.cpg, p.cpg, slice, 128) : zero);
+#pragma unroll
+        for (int g = 0; g < FEW; ++g) {
+            if (g >= p.groups)
+                break;
+            const float a = across(part[1 + g]);
             if (mine) {
                 if (p.d_gate)
                     p.d_gate[(size_t)g * p.H + out] = wp * a;
