@@ -402,18 +402,26 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
             for (int u = pair; ok && u < sh.units; u += npairs) {
                 const Unit t = unit_of(p, sh, u);
                 const int m = t.m0 + rank * 128, n = t.n0 + rank * 128;
-                constexpr int LOADS = SPLIT ? 4 : 1;          // stages of a K block
-                for (int i = 0; ok && i < (t.k1 - t.k0) * LOADS; ++i) {
-                    if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t to = base + stage * C::STAGE_BYTES;
-                    if (leader)
-                        mbar_arrive_expect_tx(full_bar(stage),
-                                              C::FEW ? C::A_BYTES + 2 * PG_B_BYTES : 2 * C::STAGE_BYTES);
-                    const uint32_t fb = full_leader0 + 8u * stage;
-                    const int k = (t.k0 + i / LOADS) * GEMM_BK;
+                for (int kb = t.k0; ok && kb < t.k1; ++kb) {
+                    const int k = kb * GEMM_BK;
+                    uint32_t to = 0, fb = 0;
+                    // the next stage, free, its bytes announced
+                    auto take = [&]() {
+                        if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag))
+                            return false;
+                        to = base + stage * C::STAGE_BYTES;
+                        fb = full_leader0 + 8u * stage;
+                        if (leader)
+                            mbar_arrive_expect_tx(full_bar(stage),
+                                                  C::FEW ? C::A_BYTES + 2 * PG_B_BYTES : 2 * C::STAGE_BYTES);
+                        issued |= 1u << stage;
+                        issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+                        if (++stage == C::STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                        return true;
+                    };
                     auto load = [&](const CUtensorMap *map, bool mn_major, int mn, int off, uint32_t dst) {
                         if (mn_major) {
 #pragma unroll
@@ -423,23 +431,22 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
                             tma_load_2d_pair(dst, map, fb, k, mn + off);
                         }
                     };
-                    if (SPLIT) {
-                        const int j = i % LOADS;
-                        const bool is_b = SPLIT == 2 ? (j & 1) : j == 0;
-                        if (is_b)
-                            load(mb, B_MN, n, p.b_off[SPLIT == 2 ? j >> 1 : 0], to);
-                        else
-                            load(ma, A_MN, m, p.a_off[SPLIT == 2 ? 1 - (j >> 1) : 3 - j], to);
-                    } else {
+                    if constexpr (SPLIT == 0) {
+                        if (!(ok = take()))
+                            break;
                         if (!C::FEW || leader)
                             load(ma, A_MN, m, p.a_off[0], to);
                         load(mb, B_MN, n, p.b_off[0], to + C::A_BYTES);
-                    }
-                    issued |= 1u << stage;
-                    issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-                    if (++stage == C::STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (!(ok = take()))
+                                break;
+                            if (SPLIT == 2 ? (j & 1) != 0 : j == 0)
+                                load(mb, B_MN, n, p.b_off[SPLIT == 2 ? j >> 1 : 0], to);
+                            else
+                                load(ma, A_MN, m, p.a_off[SPLIT == 2 ? 1 - (j >> 1) : 3 - j], to);
+                        }
                     }
                 }
             }

@@ -38,8 +38,13 @@ class MoeConfig:
     eps: float = 1e-20
 
     def c(self) -> _lib.MoeCfg:
-        return _lib.MoeCfg(self.T, self.H, self.E, self.n_group, self.topk_group, self.k, self.I, self.Is,
-                           self.rsf, self.eps)
+        # (made once: the library takes it by const pointer, and the fields never change)
+        c = self.__dict__.get("_c")
+        if c is None:
+            c = _lib.MoeCfg(self.T, self.H, self.E, self.n_group, self.topk_group, self.k, self.I, self.Is, self.rsf,
+                            self.eps)
+            object.__setattr__(self, "_c", c)
+        return c
 
     def with_T(self, T: int) -> "MoeConfig":
         return dataclasses.replace(self, T=T)
