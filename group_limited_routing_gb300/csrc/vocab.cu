@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) vocab_rows_kernel(const VocabRow
 // rows and shares their column blocks among its 1024 / R threads per row, so
 // that a few rows' many statistics are loaded at once too.  The bases are
 // log2 values, so the sums are over powers of two; pairs are joined in a fixed
-// order (a thread's own in column order, then threads by halves).
+// order (a thread's own in column order, then lanes, then warps by halves).
 template <int R>
 __global__ void __launch_bounds__(1024) vocab_join_kernel(const float2 *__restrict__ stats, int nstats, int ld,
                                                           const float *__restrict__ target_logit,
@@ -176,16 +176,22 @@ __global__ void __launch_bounds__(1024) vocab_join_kernel(const float2 *__restri
                                                           float *lse)
 {
     constexpr int SHARE = 1024 / R;
-    __shared__ float2 sm[1024];
+    __shared__ float2 sm[R][33];
     pdl_wait();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int r = threadIdx.x % R, part = threadIdx.x / R;
-    const int row = blockIdx.x * R + r;
-    const bool in = row < meta->rows;
+    const int rows = meta->rows;
+    const bool in = (int)blockIdx.x * R + r < rows;
     auto join = [](float2 a, float2 b) {
         const float top = fmaxf(a.x, b.x);
         if (!(top > -INFINITY))
             return a;
         return make_float2(top, a.y * exp2f(a.x - top) + b.y * exp2f(b.x - top));
+    };
+    auto halves = [&](float2 a, int from, int to) {
+        for (int off = from; off >= to; off >>= 1)
+            a = join(a, make_float2(__shfl_xor_sync(0xffffffffu, a.x, off), __shfl_xor_sync(0xffffffffu, a.y, off)));
+        return a;
     };
     float2 acc = make_float2(-INFINITY, 0.0f);
     if (in)
@@ -193,22 +199,24 @@ __global__ void __launch_bounds__(1024) vocab_join_kernel(const float2 *__restri
             float2 v[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                v[j] = i + j * SHARE < nstats ? stats[(size_t)(i + j * SHARE) * ld + row]
+                v[j] = i + j * SHARE < nstats ? stats[(size_t)(i + j * SHARE) * ld + blockIdx.x * R + r]
                                               : make_float2(-INFINITY, 0.0f);
             acc = join(acc, join(join(v[0], v[1]), join(v[2], v[3])));
         }
-    sm[threadIdx.x] = acc;
-    for (int half = SHARE / 2; half > 0; half >>= 1) {
-        __syncthreads();
-        if (part < half)
-            sm[threadIdx.x] = acc = join(acc, sm[threadIdx.x + half * R]);
-    }
-    if (part != 0 || !in)
+    acc = halves(acc, 16, R);              // the warp's threads of one row
+    if (lane < R)
+        sm[lane][w] = acc;
+    __syncthreads();
+    const int row = blockIdx.x * R + w;    // warp w < R: the warps' sums of row w
+    if (w >= R || row >= rows)
         return;
-    const float l = (acc.x + log2f(acc.y)) * 0.69314718055994531f;
-    const int t = row_of[row];
-    lse[t] = l;
-    loss[t] = l - target_logit[row];
+    acc = halves(sm[w][lane], 16, 1);
+    if (lane == 0) {
+        const float l = (acc.x + log2f(acc.y)) * 0.69314718055994531f;
+        const int t = row_of[row];
+        lse[t] = l;
+        loss[t] = l - target_logit[row];
+    }
 }
 
 // d_hidden[t] = bf16( scale sum_s part[s][packed row of t] ), zero where the
@@ -258,7 +266,7 @@ cudaError_t launch_vocab_join(const float2 *stats, int nstats, int ld, const flo
 {
     // 32 rows per block read whole lines; fewer rows than fill the SMs so are
     // spread, four to a block
-    const cudaError_t e = T > 4096 ? launch_pdl(vocab_join_kernel<32>, dim3((T + 31) / 32), dim3(1024), 0, s, stats,
+    const cudaError_t e = T > 2048 ? launch_pdl(vocab_join_kernel<32>, dim3((T + 31) / 32), dim3(1024), 0, s, stats,
                                                 nstats, ld, target_logit, meta, row_of, loss, lse)
                                    : launch_pdl(vocab_join_kernel<4>, dim3((T + 3) / 4), dim3(1024), 0, s, stats,
                                                 nstats, ld, target_logit, meta, row_of, loss, lse);
