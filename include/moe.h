@@ -445,7 +445,7 @@ int moe_vocab_loss(int32_t T, int32_t H, int32_t V, const moe_bf16 *hidden, cons
                    const void *target, int32_t target_bits, int64_t ignore_index, float *loss, float *lse, void *ws,
                    size_t ws_bytes, void *stream);
 
-/* Gradient of moe_vocab_loss from d_loss [T] fp32 (dL/d loss[t]; not read where
+/* Gradient of moe_vocab_loss from d_loss [T] fp32 (dL/d loss[t]; of no effect where
  * the row does not count) and the forward's lse [T]:
  *   dz[t, v] = d_loss[t] (exp(z[t, v] - lse[t]) - [v == target[t]])
  *   d_hidden [T, H] bf16 out = dz W_vocab, zero rows where the row does not count
