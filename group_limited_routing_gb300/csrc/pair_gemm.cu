@@ -59,9 +59,11 @@ template <int EPI>
 constexpr bool IS_STATS = EPI == PG_STATS || EPI == PG_STATS_FEW;
 
 // Shared memory: a ring of operand stages, and per epilogue warp the 4 KB
-// box its output leaves through (none for the statistics; two where an addend
-// arrives in them ahead of the accumulator).  A sixth stage is worth more than a
-// second box: with five, the long products of the loss's gradient took 3% more.
+// box its output leaves through (none for the statistics; two more where an
+// addend arrives, a tile ahead).  A sixth stage is worth more than a second
+// output box: with five, the long products of the loss's gradient took 3% more.
+// Storing from registers instead, without boxes and with a seventh stage, took
+// 24% more for the gradients' outputs (a warp's store then touches 32 rows).
 // PG_STATS_FEW is for at most PAIR_FEW_ROWS rows, where the product streams B
 // from memory: a stage holds those rows of A only, and the shared memory this
 // frees goes to a deeper ring of B.  The MMA still reads 128 rows per CTA; the
@@ -79,7 +81,7 @@ struct PgCfg {
     static constexpr int A_ROWS = FEW ? PAIR_FEW_ROWS : 128;
     static constexpr int A_BYTES = A_ROWS * GEMM_BK * 2;
     static constexpr int STAGE_BYTES = SPLIT ? PG_B_BYTES : A_BYTES + PG_B_BYTES;
-    static constexpr int BUFS = IS_STATS<EPI> ? 0 : EPI == PG_BF16_ADD ? 2 : 1;
+    static constexpr int BUFS = IS_STATS<EPI> ? 0 : EPI == PG_BF16_ADD ? 3 : 1;
     static constexpr int STAGING = BUFS * PG_EPI_WARPS * 4096;
     static constexpr int STAGES = (230400 - STAGING) / STAGE_BYTES;
     static constexpr int NBARS = 2 * STAGES + 2 * PG_SLOTS + 1 + PG_EPI_WARPS;
@@ -182,21 +184,6 @@ __device__ __forceinline__ void store_box(const PairGemmParams &p, uint8_t *box,
     __syncwarp();
     fill_box(box, v, lane);
     send_box<ADD>(p, box, lane, col, row);
-}
-
-// two neighbouring boxes at once (free, both of them)
-__device__ __forceinline__ void store_boxes(const PairGemmParams &p, uint8_t *boxes, const uint4 (&v)[2][8], int lane,
-                                            int col, int row)
-{
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-            *reinterpret_cast<uint4 *>(boxes + 4096 * i + lane * 128 + ((q ^ (lane & 7)) << 4)) = v[i][q];
-    fence_proxy_async_smem();
-    __syncwarp();
-    send_box<false>(p, boxes, lane, col, row);
-    send_box<false>(p, boxes + 4096, lane, col + 64, row);
 }
 
 // Softmax statistics of this lane's row over the warp's 128 columns: a base b
@@ -652,16 +639,16 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
                         break;
                     }
                     add_phase ^= 1u;
-                    // (each lane reads and then overwrites its own row of the boxes)
                     uint4 v[2][8];
                     bf16_box<true>(tacc(), empty, 1.0f, boxes, lane, v[0]);
                     bf16_box<true>(tacc() + 64, empty, 1.0f, boxes + 4096, lane, v[1]);
                     if (!empty)
                         release();
-                    store_boxes(p, boxes, v, lane, col0, row0 + p.out_row0);
-                    if (lane == 0)
-                        bulk_wait_group_read<0>();
+                    __syncwarp();                // (every lane has read its row of the boxes)
                     fetch_add(u + npairs);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        store_box<false>(p, boxes + 2 * 4096, v[i], lane, col0 + 64 * i, row0 + p.out_row0);
                 } else if constexpr (EPI == PG_BF16) {
                     uint4 v[2][8];
                     bf16_box<false>(tacc(), empty, scale, nullptr, lane, v[0]);
