@@ -35,7 +35,7 @@ const char *const kKernelNames[MOE_KERNEL_COUNT] = {
     "route_backward_d_weight", "router_plus_permute"};
 
 std::atomic<int> g_prof_on{0};
-std::atomic<int> g_inject_timeouts{0};   // test-only: gate/up GEMM launches left to sabotage
+std::atomic<int> g_inject_timeouts{0};   // test-only: GEMM launches left to sabotage
 std::mutex g_prof_mu;
 std::vector<ProfRecord> g_prof_pending;
 std::vector<cudaEvent_t> g_event_pool;
@@ -91,6 +91,8 @@ namespace glr {
 namespace host {
 
 void set_last_launches(int n) { g_last_launches = n; }
+
+bool take_injected_timeout() { return g_inject_timeouts.load() > 0 && g_inject_timeouts.fetch_sub(1) > 0; }
 
 ProfScope::ProfScope(int kid, cudaStream_t st) : on(g_prof_on.load(std::memory_order_relaxed) != 0), s(st)
 {
@@ -731,7 +733,7 @@ int forward_impl(const moe_cfg &c, const moe_bf16 *hidden, const moe_bf16 *W_gat
     p1.ld_out = c.I;
     p1.status = &hdr->status;
     p1.cap_rows = offs ? 1 : 0;
-    if (g_inject_timeouts.load() > 0 && g_inject_timeouts.fetch_sub(1) > 0) {
+    if (take_injected_timeout()) {
         p1.inject_withhold = 1;
         p1.wait_limit_ns = 50000000ull;
     }

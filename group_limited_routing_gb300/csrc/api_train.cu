@@ -47,6 +47,15 @@ NormLayout norm_layout(int T, int H, int groups)
 // ------------------------------------------------------------ dense products
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
+cudaError_t pair_product(PairEpilogue epi, PairProduct product, PairGemmParams p, int max_units, cudaStream_t s)
+{
+    if (take_injected_timeout()) {
+        p.inject_withhold = 1;
+        p.wait_limit_ns = 50000000ull;
+    }
+    return launch_pair_gemm(epi, product, p, max_units, s);
+}
+
 // K blocks per accumulator of the loss's logits (704 of K, evened out over the
 // parts): the tensor core's own running sum then stays about as close to the
 // exact one as an fp32 product's.  Measured at T = 8192, H = 2048, V = 131072,
@@ -314,7 +323,7 @@ int moe_vocab_loss(int32_t T, int32_t H, int32_t V, const moe_bf16 *hidden, cons
     p.ld_stats = T;
     p.target_logit = at<float>(ws, L.logit);
     p.status = status;
-    GLR_LAUNCH(KID_VOCAB_LOGITS, launch_pair_gemm(few ? PG_STATS_FEW : PG_STATS, PP_LOGITS, p, ceil_div(T, 256) * L.ntiles,
+    GLR_LAUNCH(KID_VOCAB_LOGITS, pair_product(few ? PG_STATS_FEW : PG_STATS, PP_LOGITS, p, ceil_div(T, 256) * L.ntiles,
                                                    s));
     GLR_LAUNCH(KID_VOCAB_JOIN, launch_vocab_join(p.stats, L.nstats, T, p.target_logit, meta, rp.row_of, T, loss, lse,
                                                  s));
@@ -426,14 +435,14 @@ int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hid
         pz.n0 = v0;
         pz.b_off[0] = v0;
         GLR_LAUNCH(KID_VOCAB_DLOGITS,
-                   launch_pair_gemm(PG_DLOGITS, PP_LOGITS, pz, m_tiles * ceil_div(n, 256), s));
+                   pair_product(PG_DLOGITS, PP_LOGITS, pz, m_tiles * ceil_div(n, 256), s));
         px.kblocks = px.part_blocks = ceil_div(n, GEMM_BK);
         px.b_off[0] = v0;
         px.accumulate = v0 > 0;
-        GLR_LAUNCH(KID_VOCAB_DX, launch_pair_gemm(PG_PARTIAL, PP_DX, px, PAIRS, s));
+        GLR_LAUNCH(KID_VOCAB_DX, pair_product(PG_PARTIAL, PP_DX, px, PAIRS, s));
         pw.M = n;
         pw.out_row0 = v0;
-        GLR_LAUNCH(KID_VOCAB_DW, launch_pair_gemm(PG_BF16, PP_DW, pw, ceil_div(n, 256) * h_tiles, s));
+        GLR_LAUNCH(KID_VOCAB_DW, pair_product(PG_BF16, PP_DW, pw, ceil_div(n, 256) * h_tiles, s));
     }
     GLR_LAUNCH(KID_VOCAB_DX, launch_vocab_dx_join(part, meta, rp.packed_of, T, H, d_hidden, s));
     set_last_launches(launches);
@@ -503,7 +512,7 @@ int moe_route_backward(const moe_cfg *cfg, const moe_bf16 *hidden, const float *
     p.status = status;
     if (d_hidden_add && !make_map_bf16(&p.tmHidden, d_hidden_add, c.T, c.H, 64, 32))
         return MOE_ERR_CUDA;
-    GLR_LAUNCH(KID_ROUTE_BWD_DX, launch_pair_gemm(d_hidden_add ? PG_BF16_ADD : PG_BF16, PP_DX_PARTS, p, ceil_div(c.T, 256) * h_tiles, s));
+    GLR_LAUNCH(KID_ROUTE_BWD_DX, pair_product(d_hidden_add ? PG_BF16_ADD : PG_BF16, PP_DX_PARTS, p, ceil_div(c.T, 256) * h_tiles, s));
     // dW = dL^T hidden, exact products: low, middle, high part of dL
     float *part = at<float>(ws, L.part);
     memset(&p, 0, sizeof(p));
@@ -524,7 +533,7 @@ int moe_route_backward(const moe_cfg *cfg, const moe_bf16 *hidden, const float *
     p.out_cols = c.H;
     p.split_rows = 256;
     p.status = status;
-    GLR_LAUNCH(KID_ROUTE_BWD_DW, launch_pair_gemm(PG_PARTIAL, PP_DW_PARTS, p, h_tiles * L.splits, s));
+    GLR_LAUNCH(KID_ROUTE_BWD_DW, pair_product(PG_PARTIAL, PP_DW_PARTS, p, h_tiles * L.splits, s));
     if (L.splits > 1)
         GLR_LAUNCH(KID_ROUTE_BWD_DW, launch_sum_splits(part, L.splits, 256ll * c.H, (long long)c.E * c.H, dW_router, s));
     set_last_launches(launches);

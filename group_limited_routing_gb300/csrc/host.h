@@ -22,6 +22,9 @@ enum KernelId {
     KID_STAGE_ROUTE_PERMUTE   // (per-stage timing) the routing and bucketing kernels as one interval
 };
 
+// whether a launch is to be sabotaged (moe_debug_inject_timeout); counts it
+bool take_injected_timeout();
+
 // kernels the last call of this thread enqueued (moe_last_launch_count)
 void set_last_launches(int n);
 

@@ -424,6 +424,9 @@ struct PairGemmParams {
     float *target_logit;      // per packed row
     const float *lse, *weight; // per packed row
     int *status;
+    // fault injection for tests: the loader issues nothing, waits give up after wait_limit_ns
+    int inject_withhold;
+    unsigned long long wait_limit_ns;   // 0: the default
 };
 // The operands of a product: rows of K (A, B as nn.Linear has them), B as rows
 // of N, both as rows of M and N (a gradient's transposed operand); with parts,

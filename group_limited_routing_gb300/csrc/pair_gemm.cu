@@ -383,6 +383,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
     const int pair = (int)blockIdx.x / 2;
     const Shape sh = shape_of(p);
     const bool packed = p.meta && p.meta->rows < p.T;
+    const unsigned long long limit = p.wait_limit_ns ? p.wait_limit_ns : WAIT_LIMIT_NS;
     bool aborted_peer_loads = false;
 
     if (warp == 0) {
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
             const uint32_t full_leader0 = mapa_shared(full_bar(0), 0);
             int stage = 0;
             uint32_t phase = 0, issued = 0, issued_parity = 0;
-            bool ok = true;
+            bool ok = !p.inject_withhold;
             for (int u = pair; ok && u < sh.units; u += npairs) {
                 const Unit t = unit_of(p, sh, u);
                 const int m = t.m0 + rank * 128, n = t.n0 + rank * 128;
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
                     uint32_t to = 0, fb = 0;
                     // the next stage, free, its bytes announced
                     auto take = [&]() {
-                        if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag))
+                        if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, limit))
                             return false;
                         to = base + stage * C::STAGE_BYTES;
                         fb = full_leader0 + 8u * stage;
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
                     const int kp = t.k0 + part * p.part_blocks, ke = min(kp + p.part_blocks, t.k1);
                     const uint32_t slot = ctr % PG_SLOTS, par = (ctr / PG_SLOTS) & 1u;
                     // (the peer's epilogue warps arrive here across the pair)
-                    if (!mbar_wait_cluster(tempty0 + 8u * slot, par ^ 1u, abort_flag)) {
+                    if (!mbar_wait_cluster(tempty0 + 8u * slot, par ^ 1u, abort_flag, limit)) {
                         ok = false;
                         break;
                     }
@@ -476,7 +477,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
                     // the next stage, once its bytes are there (0: gave up)
                     auto take = [&](int &st) {
                         st = stage;
-                        if (!mbar_wait(full_bar(stage), phase, abort_flag))
+                        if (!mbar_wait(full_bar(stage), phase, abort_flag, limit))
                             return false;
                         tc_fence_after();
                         if (++stage == C::STAGES) {
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
         auto accumulator = [&]() {
             int got = 1;
             if (lane == 0)
-                got = mbar_wait(tfull0 + 8u * (ctr % PG_SLOTS), (ctr / PG_SLOTS) & 1u, abort_flag) ? 1 : 0;
+                got = mbar_wait(tfull0 + 8u * (ctr % PG_SLOTS), (ctr / PG_SLOTS) & 1u, abort_flag, limit) ? 1 : 0;
             got = __shfl_sync(0xffffffffu, got, 0);
             __syncwarp();
             tc_fence_after();
@@ -629,7 +630,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
                 if constexpr (EPI == PG_BF16_ADD) {
                     int got = 1;
                     if (lane == 0) {
-                        got = mbar_wait(add_bar, add_phase, abort_flag) ? 1 : 0;
+                        got = mbar_wait(add_bar, add_phase, abort_flag, limit) ? 1 : 0;
                         add_pending = got == 0;
                     }
                     got = __shfl_sync(0xffffffffu, got, 0);

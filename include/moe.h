@@ -508,7 +508,8 @@ int moe_profile_read(int kernel_id, double *total_ms, int32_t *launches, int res
 const char *moe_kernel_name(int kernel_id);
 
 /* Fault injection for tests of the failure path (no counterpart on the pages).
- * The next `launches` grouped gate/up GEMM launches made by moe_forward, in
+ * The next `launches` grouped gate/up GEMM launches made by moe_forward, or
+ * products launched by moe_vocab_loss, its backward and moe_route_backward, in
  * this process, run with their TMA producer withholding every load and a
  * 50 ms wait limit: the MMA lane's first wait runs out, the kernel winds down
  * (copies drained, TMEM freed) and sets MOE_STATUS_TIMEOUT; the call's output
