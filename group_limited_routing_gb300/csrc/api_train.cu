@@ -135,9 +135,22 @@ bool vocab_logits_maps(PairGemmParams &p, const VocabLayout &L, int T, int H, in
 
 // ------------------------------------------------------- the router's gradient
 struct RouteBwdLayout {
-    size_t split, parts, part, total;
+    size_t split, parts, part, logits, total;
     int splits;
+    int logit_splits;          // 0: the logits come from the forward's router
 };
+
+// The logits again.  The forward's router keeps one accumulator over its part of
+// K, whose additions the tensor core truncates: that is most of the error of
+// d_W_router (relative 2-norm 1.1e-6 at H = 2048, at any T).  A batch of one tile
+// of rows (and more than the CUDA-core router takes) forms the logits with the
+// pair product instead, the hidden rows against the weight's three parts, K cut
+// into splits for the SMs and into accumulators of ROUTE_LOGIT_BLOCKS blocks that
+// are added in fp32 registers: 3.4e-7, what an fp32 product on the CUDA cores has.
+// It costs 3 us (T = 104: 35.5 against 32.6, T = 4096: 58.8 against 56.0, E = 256,
+// 4 blocks per accumulator: 35.3 and 9.0e-7); from 256 rows up a library's fp32
+// product is at 1.0e-6 as well, and the forward's router serves.
+constexpr int ROUTE_PAIR_LOGITS_MAX_T = 256, ROUTE_LOGIT_BLOCKS = 2;
 
 // 64-token blocks per accumulator of the weight gradient (its K is the tokens)
 constexpr int ROUTE_DW_BLOCKS = 4;
@@ -155,6 +168,11 @@ RouteBwdLayout route_bwd_layout(const moe_cfg &c)
     L.parts = take(3ull * c.T * c.E * 2);
     L.splits = choose_splits(ceil_div(c.H, 256), 3 * ceil_div(c.T, GEMM_BK), 256ll * c.H, 64, 3);
     L.part = take(L.splits > 1 ? 4ull * L.splits * 256 * c.H : 0);
+    L.logit_splits = 0;
+    if (c.T > ROUTER_SIMT_MAX_T && c.T <= ROUTE_PAIR_LOGITS_MAX_T) {
+        L.logit_splits = choose_splits(1, 3 * (c.H / GEMM_BK), 256ll * c.E, 8, 6);
+        L.logits = take(4ull * L.logit_splits * 256 * c.E);
+    }
     L.total = off;
     return L;
 }
@@ -487,11 +505,37 @@ int moe_route_backward(const moe_cfg *cfg, const moe_bf16 *hidden, const float *
     }
     float *logits = nullptr;
     int nparts = 1;
-    if ((rc = route_region_logits(c, hidden, W_router, W3, ws, sms, s, launches, &logits, &nparts)) != MOE_OK)
+    long long part_stride = (long long)c.T * c.E;
+    if (L.logit_splits) {
+        logits = at<float>(ws, L.logits);
+        nparts = L.logit_splits;
+        const int rows = 256;
+        part_stride = (long long)rows * c.E;
+        PairGemmParams p;
+        memset(&p, 0, sizeof(p));
+        if (!make_map_bf16(&p.tmA, hidden, c.T, c.H, GEMM_BK, 128) ||
+            !make_map_bf16(&p.tmB, W3, 3ull * c.E, c.H, GEMM_BK, 128) ||
+            !make_map_f32(&p.tmOut, logits, (uint64_t)nparts * rows, c.E, 32, 32))
+            return MOE_ERR_CUDA;
+        p.M = c.T;
+        p.N = c.E;
+        p.kblocks = c.H / GEMM_BK;
+        p.part_blocks = ROUTE_LOGIT_BLOCKS;
+        p.b_off[1] = c.E;
+        p.b_off[2] = 2 * c.E;
+        p.splits = nparts;
+        p.group_m = 1;
+        p.out_rows = nparts * rows;
+        p.out_cols = c.E;
+        p.split_rows = rows;
+        p.status = status;
+        GLR_LAUNCH(KID_ROUTER_GEMM, pair_product(PG_PARTIAL, PP_LOGITS_PARTS, p, nparts, s));
+    } else if ((rc = route_region_logits(c, hidden, W_router, W3, ws, sms, s, launches, &logits, &nparts)) != MOE_OK) {
         return rc;
+    }
     uint16_t *parts = at<uint16_t>(ws, L.parts);
-    GLR_LAUNCH(KID_ROUTE_BWD_SCORES, launch_route_grad(logits, nparts, topk_idx, d_topk_w, expert_counts, d_aux_loss, c.T, c.E,
-                                                       c.k, c.rsf, c.eps, parts, status, s));
+    GLR_LAUNCH(KID_ROUTE_BWD_SCORES, launch_route_grad(logits, nparts, part_stride, topk_idx, d_topk_w, expert_counts,
+                                                       d_aux_loss, c.T, c.E, c.k, c.rsf, c.eps, parts, status, s));
     const int h_tiles = ceil_div(c.H, 256);
     // d_hidden = dL W: of the parts' products the three largest (the rest is
     // below 2^-16 of the result, which is rounded to bf16)

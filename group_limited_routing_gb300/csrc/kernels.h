@@ -408,7 +408,7 @@ struct PairGemmParams {
     int k_from_rows;          // K = meta->rows
     int M, N;
     int kblocks;              // K in blocks of 64
-    int a_off[3], b_off[2];   // rows added to the operand's row coordinate (of each part)
+    int a_off[3], b_off[3];   // rows added to the operand's row coordinate (of each part)
     int splits;               // K range cut among this many units; 0: meta->splits
     int part_blocks;          // K blocks per accumulator (STATS, PARTIAL; else at least kblocks)
     int group_m;              // tiles run m-fastest within groups of this many m-tiles
@@ -430,9 +430,9 @@ struct PairGemmParams {
 };
 // The operands of a product: rows of K (A, B as nn.Linear has them), B as rows
 // of N, both as rows of M and N (a gradient's transposed operand); with parts,
-// the fp32 operands as bf16 parts stacked along their rows (A and B in two each;
-// A in three).
-enum PairProduct { PP_LOGITS = 0, PP_DX = 1, PP_DW = 2, PP_DX_PARTS = 3, PP_DW_PARTS = 4 };
+// the fp32 operands as bf16 parts stacked along their rows (B in three; A and B
+// in two each; A in three).
+enum PairProduct { PP_LOGITS = 0, PP_DX = 1, PP_DW = 2, PP_DX_PARTS = 3, PP_DW_PARTS = 4, PP_LOGITS_PARTS = 5 };
 cudaError_t launch_pair_gemm(PairEpilogue epi, PairProduct product, const PairGemmParams &p, int max_units,
                              cudaStream_t s);
 
@@ -463,10 +463,10 @@ cudaError_t launch_vocab_dx_join(const float *part, const VocabMeta *meta, const
                                  uint16_t *d_hidden, cudaStream_t s);
 
 // ---- the router's gradient (route_grad.cu) --------------------------------------
-// (logits: nparts buffers of [T, E], one after the other, to be added)
-cudaError_t launch_route_grad(const float *logits, int nparts, const int32_t *idx, const float *d_w, const int32_t *counts,
-                              const float *d_aux, int T, int E, int k, float rsf, float eps, uint16_t *parts,
-                              int *status, cudaStream_t s);
+// (logits: nparts buffers of [T, E], part_stride floats apart, to be added)
+cudaError_t launch_route_grad(const float *logits, int nparts, long long part_stride, const int32_t *idx,
+                              const float *d_w, const int32_t *counts, const float *d_aux, int T, int E, int k, float rsf,
+                              float eps, uint16_t *parts, int *status, cudaStream_t s);
 // out[i] = sum over the splits of part[s stride + i], i < n
 cudaError_t launch_sum_splits(const float *part, int splits, long long stride, long long n, float *out,
                               cudaStream_t s);

@@ -75,6 +75,7 @@ constexpr bool IS_STATS = EPI == PG_STATS || EPI == PG_STATS_FEW;
 //   2: the parts in order A middle, B high, A high, B middle, and the products
 //      middle x high, high x high, high x middle
 //   3: B, A low, A middle, A high, and each A x B as its A arrives
+//   1: the same with the operands' roles exchanged
 template <int EPI, int SPLIT>
 struct PgCfg {
     static constexpr bool FEW = EPI == PG_STATS_FEW;
@@ -438,10 +439,10 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
                         for (int j = 0; j < 4; ++j) {
                             if (!(ok = take()))
                                 break;
-                            if (SPLIT == 2 ? (j & 1) != 0 : j == 0)
-                                load(mb, B_MN, n, p.b_off[SPLIT == 2 ? j >> 1 : 0], to);
+                            if (SPLIT == 2 ? (j & 1) != 0 : (j == 0) == (SPLIT == 3))
+                                load(mb, B_MN, n, p.b_off[SPLIT == 2 ? j >> 1 : SPLIT == 3 ? 0 : 3 - j], to);
                             else
-                                load(ma, A_MN, m, p.a_off[SPLIT == 2 ? 1 - (j >> 1) : 3 - j], to);
+                                load(ma, A_MN, m, p.a_off[SPLIT == 2 ? 1 - (j >> 1) : SPLIT == 1 ? 0 : 3 - j], to);
                         }
                     }
                 }
@@ -508,24 +509,28 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
                         } else {
                             if (!(ok = take(s0) && take(s1)))
                                 break;
-                            if (SPLIT == 2)
-                                multiply(at(s0), at(s1), kb == kp);   // A middle, B high
-                            else
+                            if (SPLIT == 3)
                                 multiply(at(s1), at(s0), kb == kp);   // A low, B
+                            else
+                                multiply(at(s0), at(s1), kb == kp);   // A middle, B high (A, B low)
                             umma_commit_pair(empty_bar(SPLIT == 2 ? s0 : s1), 0x3);
                             if (!(ok = take(s2)))
                                 break;
                             if (SPLIT == 2)
                                 multiply(at(s2), at(s1), false);      // A high, B high
-                            else
+                            else if (SPLIT == 3)
                                 multiply(at(s2), at(s0), false);      // A middle, B
+                            else
+                                multiply(at(s0), at(s2), false);      // A, B middle
                             umma_commit_pair(empty_bar(SPLIT == 2 ? s1 : s2), 0x3);
                             if (!(ok = take(s3)))
                                 break;
                             if (SPLIT == 2)
                                 multiply(at(s2), at(s3), false);      // A high, B middle
-                            else
+                            else if (SPLIT == 3)
                                 multiply(at(s3), at(s0), false);      // A high, B
+                            else
+                                multiply(at(s0), at(s3), false);      // A, B high
                             umma_commit_pair(empty_bar(SPLIT == 2 ? s2 : s0), 0x3);
                             umma_commit_pair(empty_bar(s3), 0x3);
                         }
@@ -751,6 +756,10 @@ cudaError_t launch_pair_gemm(PairEpilogue epi, PairProduct product, const PairGe
     case PP_DW:
         if (epi == PG_BF16)
             return launch_one<PG_BF16, true, true>(p, max_units, s);
+        break;
+    case PP_LOGITS_PARTS:
+        if (epi == PG_PARTIAL)
+            return launch_one<PG_PARTIAL, false, false, 1>(p, max_units, s);
         break;
     case PP_DX_PARTS:
         if (epi == PG_BF16)

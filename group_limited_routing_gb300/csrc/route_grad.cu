@@ -40,6 +40,7 @@ __device__ __forceinline__ float warp_sum(float v)
 // One warp per token; a lane holds EPL = E / 32 neighbouring experts.
 template <int EPL>
 __global__ void __launch_bounds__(256) route_grad_kernel(const float *__restrict__ logits, int nparts,
+                                                         long long stride,
                                                          const int32_t *__restrict__ idx,
                                                          const float *__restrict__ d_w,
                                                          const int32_t *__restrict__ counts,
@@ -52,7 +53,6 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const float *__restrict
     pdl_trigger();
     const int lane = threadIdx.x & 31;
     const int warps = gridDim.x * (blockDim.x >> 5);
-    const long long stride = (long long)T * E;
     float f[EPL];
     const float aux = d_aux ? *d_aux * ((float)E / (float)T) : 0.0f;
 #pragma unroll
@@ -197,16 +197,16 @@ __global__ void __launch_bounds__(256) sum_splits_kernel(const float *__restrict
     reinterpret_cast<float4 *>(out)[i] = a;
 }
 
-cudaError_t launch_route_grad(const float *logits, int nparts, const int32_t *idx, const float *d_w, const int32_t *counts,
-                              const float *d_aux, int T, int E, int k, float rsf, float eps, uint16_t *parts,
-                              int *status, cudaStream_t s)
+cudaError_t launch_route_grad(const float *logits, int nparts, long long part_stride, const int32_t *idx,
+                              const float *d_w, const int32_t *counts, const float *d_aux, int T, int E, int k, float rsf,
+                              float eps, uint16_t *parts, int *status, cudaStream_t s)
 {
     const int want = (T + 7) / 8, most = 152 * 5;      // (what the SMs hold at once)
     const dim3 grid(want < most ? want : most);
-    const cudaError_t e = E == 256 ? launch_pdl(route_grad_kernel<8>, grid, dim3(256), 0, s, logits, nparts, idx, d_w, counts,
-                                                d_aux, T, k, rsf, eps, parts, status)
-                                   : launch_pdl(route_grad_kernel<4>, grid, dim3(256), 0, s, logits, nparts, idx, d_w, counts,
-                                                d_aux, T, k, rsf, eps, parts, status);
+    const cudaError_t e = E == 256 ? launch_pdl(route_grad_kernel<8>, grid, dim3(256), 0, s, logits, nparts, part_stride,
+                                                idx, d_w, counts, d_aux, T, k, rsf, eps, parts, status)
+                                   : launch_pdl(route_grad_kernel<4>, grid, dim3(256), 0, s, logits, nparts, part_stride,
+                                                idx, d_w, counts, d_aux, T, k, rsf, eps, parts, status);
     return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
 

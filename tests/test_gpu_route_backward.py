@@ -90,6 +90,19 @@ def test_formula(T, H, E, k, aux, add):
     check(cfg, d, got, aux, add)
 
 
+@pytest.mark.parametrize("T,H,E,k", [(34, 64, 128, 2), (100, 7168, 256, 8), (250, 1472, 256, 8), (255, 128, 128, 8),
+                                     (256, 2048, 256, 8)])
+def test_one_tile_of_rows(T, H, E, k):
+    """Batches of at most 256 tokens form the logits a way of their own; the same
+    bits with a prepared weight."""
+    cfg, d = inputs(T, H, E, k, seed=3 * T + H)
+    got, ws = run(cfg, d, True, True)
+    assert ws.status() == 0
+    check(cfg, d, got, True, True)
+    again, _ = run(cfg, d, True, True, W_split=moe.prepare_router(cfg, d["W"]))
+    assert all(torch.equal(got[n], again[n]) for n in ("d_hidden", "dW_router"))
+
+
 def test_many_experts_per_token():
     cfg, d = inputs(300, 256, 256, 32, seed=5, keep=8)
     check(cfg, d, run(cfg, d, True, False)[0], True, False)
