@@ -546,8 +546,9 @@ def block_norm_backward(x, y, gate, w_post, w_pre, d_r, d_n, *, alpha: float = 1
     for name, (shape, dt) in shapes.items():
         t = out.get(name) if out else None
         if t is None:
-            t = torch.empty(*shape, dtype=dt, device=dev)
-        _need(t, name, dt, shape, dev)
+            t = torch.empty(shape, dtype=dt, device=dev)
+        else:
+            _need(t, name, dt, shape, dev)
         g[name] = t
     need = int(_lib.load().moe_block_norm_workspace_bytes(T, H, groups))
     if need and (ws is None or ws.nbytes < need):
