@@ -36,7 +36,7 @@
 // Measured on one GB300 (copy rate 6.79 TB/s): T = 32768, H = 2048 in bf16
 // forward 92 us, 5.8 TB/s (0.86 of the copy rate); backward with the column sums
 // 150 us, 5.4 TB/s (0.79), its two reductions per row and their barriers being
-// the rest; T = 4095, H = 1536, fp32 stream, backward 40 us (0.41: five rows per
+// the rest; T = 4095, H = 1536, fp32 stream, backward 39 us (0.43: five rows per
 // block do not outlast a block's start and the column sums' kernel).
 #include <cuda_bf16.h>
 
@@ -689,15 +689,19 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const BlockNor
 
 // The column sums from the chunks' and blocks' partial sums, in a fixed order:
 // dw_pre = sum_b B[b], d_gate[g] = w_post sum_c A[g, c], dw_post = sum_g gate[g]
-// sum_c A[g, c].  A block takes 32 columns: 8 threads of four columns each, 128
-// partial sums at a time, all loads of a thread in flight at once.
-__global__ void __launch_bounds__(1024) block_norm_finish_kernel(const BlockNormParams p, int blocks)
+// sum_c A[g, c].  A block takes FIN_COLS columns: FIN_LANES threads of four
+// columns each (a sector of a row), FIN_SLICES partial sums at a time, all loads of
+// a thread in flight at once.  32 columns and 1024 threads left most SMs idle: the
+// whole backward 40.1 against 39.0 us at T = 4095, H = 1536; 16 columns 39.6.
+constexpr int FIN_COLS = 8, FIN_THREADS = 512;
+constexpr int FIN_LANES = FIN_COLS / 4, FIN_SLICES = FIN_THREADS / FIN_LANES, FIN_WARPS = FIN_THREADS / 32;
+__global__ void __launch_bounds__(FIN_THREADS) block_norm_finish_kernel(const BlockNormParams p, int blocks)
 {
-    __shared__ float sm[32][32];
+    __shared__ __align__(16) float sm[FIN_WARPS][FIN_COLS];
     pdl_wait();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int col = (lane & 7) * 4, slice = w * 4 + (lane >> 3);
-    const int h = blockIdx.x * 32 + col;
+    const int col = (lane % FIN_LANES) * 4, slice = threadIdx.x / FIN_LANES;
+    const int h = blockIdx.x * FIN_COLS + col;
     const bool in = h < p.H;                      // (H is a multiple of 8)
     auto add = [](float4 &a, const float4 &b) { a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w; };
     // sum of partial sums row0 .. row0 + n - 1 by `many` slices, this thread being number `at` of them
@@ -708,36 +712,36 @@ __global__ void __launch_bounds__(1024) block_norm_finish_kernel(const BlockNorm
             add(a, *reinterpret_cast<const float4 *>(part + (row0 + i) * p.H + h));
         return a;
     };
-    // the warp's four slices, then the 32 warps in order; warp 0 lanes 0..31 get column `lane`
+    // the warp's slices, then the warps in order; warp 0's first lanes get column `lane`
     auto across = [&](float4 a) {
 #pragma unroll
-        for (int off = 8; off <= 16; off <<= 1) {
+        for (int off = FIN_LANES; off <= 16; off <<= 1) {
             a.x += __shfl_xor_sync(0xffffffffu, a.x, off);
             a.y += __shfl_xor_sync(0xffffffffu, a.y, off);
             a.z += __shfl_xor_sync(0xffffffffu, a.z, off);
             a.w += __shfl_xor_sync(0xffffffffu, a.w, off);
         }
         __syncthreads();
-        if (lane < 8)
+        if (lane < FIN_LANES)
             *reinterpret_cast<float4 *>(&sm[w][col]) = a;
         __syncthreads();
         float t = 0.0f;
-        if (w == 0)
+        if (w == 0 && lane < FIN_COLS)
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < FIN_WARPS; ++i)
                 t += sm[i][lane];
         return t;
     };
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int out = blockIdx.x * 32 + lane;       // warp 0's column
-    const bool mine = w == 0 && out < p.H;
+    const int out = blockIdx.x * FIN_COLS + lane; // warp 0's column
+    const bool mine = w == 0 && lane < FIN_COLS && out < p.H;
     constexpr int FEW = 4;
     const bool few = p.part_a && p.groups <= FEW;  // a few long groups: the whole block takes each
     float4 part[1 + FEW];
-    part[0] = in ? some(p.part_b, 0, blocks, slice, 128) : zero;
+    part[0] = in ? some(p.part_b, 0, blocks, slice, FIN_SLICES) : zero;
 #pragma unroll
     for (int g = 0; g < FEW; ++g)
-        part[1 + g] = in && few && g < p.groups ? some(p.part_a, (size_t)g * p.cpg, p.cpg, slice, 128) : zero;
+        part[1 + g] = in && few && g < p.groups ? some(p.part_a, (size_t)g * p.cpg, p.cpg, slice, FIN_SLICES) : zero;
     const float pre = across(part[0]);
     if (mine && p.dw_pre)
         p.dw_pre[out] = pre;
@@ -766,7 +770,7 @@ __global__ void __launch_bounds__(1024) block_norm_finish_kernel(const BlockNorm
     if (in && p.w_post)
         wp = *reinterpret_cast<const float4 *>(p.w_post + h);
     if (in)
-        for (int g = slice; g < p.groups; g += 128) {
+        for (int g = slice; g < p.groups; g += FIN_SLICES) {
             const float4 a = some(p.part_a, (size_t)g * p.cpg, p.cpg, 0, 1);
             const size_t at = (size_t)g * p.H + h;
             if (p.d_gate) {
@@ -916,7 +920,8 @@ cudaError_t launch_block_norm_backward(const BlockNormParams &p, bool stream_f32
 
 cudaError_t launch_block_norm_finish(const BlockNormParams &p, int blocks, cudaStream_t s)
 {
-    const cudaError_t e = launch_pdl(block_norm_finish_kernel, dim3((p.H + 31) / 32), dim3(1024), 0, s, p, blocks);
+    const cudaError_t e = launch_pdl(block_norm_finish_kernel, dim3((p.H + FIN_COLS - 1) / FIN_COLS),
+                                     dim3(FIN_THREADS), 0, s, p, blocks);
     return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
 
