@@ -430,6 +430,7 @@ int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hid
     px.group_m = 1;
     px.out_rows = L.part_rows;
     px.out_cols = H;
+    px.beside = PG_FIRST;
     px.status = status;
     // dW piece = dz^T hidden
     memset(&pw, 0, sizeof(pw));
@@ -446,6 +447,7 @@ int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hid
     pw.group_m = 1;
     pw.out_rows = V;
     pw.out_cols = H;
+    pw.beside = PG_SECOND;
     pw.status = status;
     for (int v0 = 0; v0 < V; v0 += L.piece) {
         const int n = std::min(L.piece, V - v0);
@@ -553,6 +555,7 @@ int moe_route_backward(const moe_cfg *cfg, const moe_bf16 *hidden, const float *
     p.group_m = 1;
     p.out_rows = c.T;
     p.out_cols = c.H;
+    p.beside = PG_FIRST;
     p.status = status;
     if (d_hidden_add && !make_map_bf16(&p.tmHidden, d_hidden_add, c.T, c.H, 64, 32))
         return MOE_ERR_CUDA;
@@ -576,6 +579,7 @@ int moe_route_backward(const moe_cfg *cfg, const moe_bf16 *hidden, const float *
     p.out_rows = L.splits == 1 ? c.E : 256 * L.splits;
     p.out_cols = c.H;
     p.split_rows = 256;
+    p.beside = PG_SECOND;
     p.status = status;
     GLR_LAUNCH(KID_ROUTE_BWD_DW, pair_product(PG_PARTIAL, PP_DW_PARTS, p, h_tiles * L.splits, s));
     if (L.splits > 1)

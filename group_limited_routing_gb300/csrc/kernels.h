@@ -19,7 +19,8 @@ namespace glr {
 // processing and (for the GEMMs) its prologue overlap this one's teardown.
 // (Triggering at the start of each CTA was measured slower: the dependents'
 // waiting CTAs then sit beside the running ones.)  Since every kernel waits,
-// completion stays ordered along the whole stream.
+// completion stays ordered along the whole stream; the second of two products
+// that run beside each other (PairBeside) waits at its end instead.
 __device__ __forceinline__ void pdl_wait()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -397,6 +398,12 @@ struct VocabMeta {
 };
 constexpr int VOCAB_MAX_SPLITS = 16, VOCAB_MIN_SPLIT_BLOCKS = 8;
 
+// Two products of which neither reads or writes what the other writes: the
+// second's blocks come up as the first's leave their SMs (a gradient's two
+// products: router, T = 128 33.0 -> 31.2 us, T = 32768 236 -> 232; loss, T = 1021
+// 233 -> 229).
+enum PairBeside { PG_ALONE = 0, PG_FIRST = 1, PG_SECOND = 2 };
+
 struct PairGemmParams {
     CUtensorMap tmA, tmB, tmOut;
     // the rows that count, packed: replaces A (STATS, DLOGITS) or B (BF16) when
@@ -411,6 +418,7 @@ struct PairGemmParams {
     int a_off[3], b_off[3];   // rows added to the operand's row coordinate (of each part)
     int splits;               // K range cut among this many units; 0: meta->splits
     int part_blocks;          // K blocks per accumulator (STATS, PARTIAL; else at least kblocks)
+    int beside;               // PairBeside
     int group_m;              // tiles run m-fastest within groups of this many m-tiles
     int out_row0;             // row of the output map where row 0 goes
     int out_rows, out_cols;   // the output map's extent

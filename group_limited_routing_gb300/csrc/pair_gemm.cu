@@ -378,7 +378,13 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
     cluster_sync();            // both CTAs' barriers initialised and TMEM allocated
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    pdl_wait();                // operands and row counts come from earlier kernels
+    // Operands and row counts come from earlier kernels; of a product beside the one
+    // launched before it, from the kernels that that one waited for before it let
+    // this one start (so this one need only outlast it).
+    if (p.beside != PG_SECOND)
+        pdl_wait();
+    if (p.beside == PG_FIRST)
+        pdl_trigger();
 
     const int npairs = (int)gridDim.x / 2;
     const int pair = (int)blockIdx.x / 2;
@@ -684,6 +690,8 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
         while (globaltimer_ns() - t0 < 100000ull) {
         }
     }
+    if (p.beside == PG_SECOND)
+        pdl_wait();
     tc_fence_before();
     cluster_sync();
     if (warp == 1) {
