@@ -485,6 +485,14 @@ def rmsnorm(x, eps: float = 1e-6, out=None):
     return out
 
 
+def _sized(ws: Optional[SizedWorkspace], need: int, what: str, device) -> Optional[SizedWorkspace]:
+    """ws, or one of `need` bytes where none was given.  One that is too small is
+    refused: its owner would look for the call's status in it."""
+    if ws is not None and ws.nbytes < need:
+        raise ValueError("workspace too small for %s: %d bytes, needs %d" % (what, ws.nbytes, need))
+    return SizedWorkspace(need, what, device) if ws is None and need else ws
+
+
 def block_norm_workspace(T: int, H: int, groups: int = 1, device=None) -> SizedWorkspace:
     """The workspace of block_norm_backward."""
     return SizedWorkspace(_lib.load().moe_block_norm_workspace_bytes(T, H, groups), "moe_block_norm_backward", device)
@@ -551,8 +559,7 @@ def block_norm_backward(x, y, gate, w_post, w_pre, d_r, d_n, *, alpha: float = 1
             _need(t, name, dt, shape, dev)
         g[name] = t
     need = int(_lib.load().moe_block_norm_workspace_bytes(T, H, groups))
-    if need and (ws is None or ws.nbytes < need):
-        ws = SizedWorkspace(need, "moe_block_norm_backward", dev)
+    ws = _sized(ws, need, "moe_block_norm_backward", dev)
     # (an unsupported shape has no workspace size: the call itself names the error)
     ptr = {name: t.data_ptr() for name, t in g.items()}
     rc = _lib.load().moe_block_norm_backward(T, H, groups, f32, px, py, pg, pp, pq, alpha, eps, pdr, pdn, ptr["d_x"],
@@ -581,8 +588,7 @@ def _vocab_args(hidden, W_vocab, target, backward, ws):
         raise TypeError("target must be a torch.int32 or torch.int64 tensor")
     pt = _need(target, "target", target.dtype, (T,), dev)
     need = int(_lib.load().moe_vocab_loss_workspace_bytes(T, H, V, int(backward)))
-    if need and (ws is None or ws.nbytes < need):
-        ws = SizedWorkspace(need, "moe_vocab_loss", dev)
+    ws = _sized(ws, need, "moe_vocab_loss", dev)
     # (an unsupported shape has no workspace size: the call itself names the error;
     # the caller holds on to ws until the launches are enqueued)
     bits = 64 if target.dtype == torch.int64 else 32
@@ -657,8 +663,7 @@ def route_backward(cfg: MoeConfig, hidden, W_router, topk_idx, d_topk_w, *, d_au
         _need(t, name, dt, shape, dev)
         g[name] = t
     need = int(_lib.load().moe_route_backward_workspace_bytes(ctypes.byref(cfg.c())))
-    if need and (ws is None or ws.nbytes < need):
-        ws = SizedWorkspace(need, "moe_route_backward", dev)
+    ws = _sized(ws, need, "moe_route_backward", dev)
     rc = _lib.load().moe_route_backward(ctypes.byref(cfg.c()), ph, pw, ps, pi, pd, pc, pa, pp,
                                         g["d_hidden"].data_ptr(), g["dW_router"].data_ptr(),
                                         ws.ptr if need else None, ws.nbytes if need else 0, _stream(dev))
