@@ -608,7 +608,9 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
                         ok = false;
                         break;
                     }
-                    if (part == 0) {
+                    if (IS_STATS<EPI> && row0 >= sh.M) {
+                        // (a short tile's empty rows)
+                    } else if (part == 0) {
 #pragma unroll
                         for (int c = 0; c < PG_HALF; c += 32)
                             tmem_load32(tacc() + c, z + c);
