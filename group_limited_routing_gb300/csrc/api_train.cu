@@ -87,6 +87,7 @@ constexpr size_t VOCAB_PIECE_BYTES = 1ull << 30;
 struct VocabLayout {
     size_t meta, row_of, target, packed_of, lse, weight, logit, stats, hidden, dz, part, total;
     int ntiles, nstats, piece, part_rows;
+    int rows;                  // packed rows at most: T, or the repeated ones of a few
 };
 
 VocabLayout vocab_layout(int T, int H, int V, bool backward)
@@ -101,20 +102,21 @@ VocabLayout vocab_layout(int T, int H, int V, bool backward)
     };
     L.ntiles = ceil_div(V, 256);
     L.nstats = ceil_div(V, 128);
+    L.rows = backward ? std::max(T, 2 * std::min(T, VOCAB_TWICE_ROWS)) : T;
     L.meta = take(sizeof(VocabMeta));
     L.row_of = take(4ull * T);
-    L.target = take(4ull * T);
-    L.hidden = take(2ull * T * H);
+    L.target = take(4ull * L.rows);
+    L.hidden = take(2ull * L.rows * H);
     if (backward) {
         L.packed_of = take(4ull * T);
-        L.lse = take(4ull * T);
-        L.weight = take(4ull * T);
-        const size_t most = std::max<size_t>(1, VOCAB_PIECE_BYTES / (512ull * T));   // 256-column blocks
+        L.lse = take(4ull * L.rows);
+        L.weight = take(4ull * L.rows);
+        const size_t most = std::max<size_t>(1, VOCAB_PIECE_BYTES / (512ull * L.rows));   // 256-column blocks
         L.piece = (int)std::min<size_t>(L.ntiles, most) * 256;
-        L.dz = take(2ull * T * L.piece);
+        L.dz = take(2ull * L.rows * L.piece);
         // fp32 sums of d_hidden: one slice per split, and as few rows as count
         // (which the host does not know) may be split the most
-        const int h_tiles = ceil_div(H, 256), m_tiles = ceil_div(T, 256);
+        const int h_tiles = ceil_div(H, 256), m_tiles = ceil_div(L.rows, 256);
         L.part_rows = 256 * std::max(m_tiles, std::min(VOCAB_MAX_SPLITS * m_tiles, SPLIT_MAX_UNITS / h_tiles));
         L.part = take(4ull * L.part_rows * H);
     } else {
@@ -134,7 +136,7 @@ bool vocab_logits_maps(PairGemmParams &p, const VocabLayout &L, int T, int H, in
                        const moe_bf16 *W, void *ws, int a_rows)
 {
     return make_map_bf16(&p.tmA, hidden, T, H, GEMM_BK, a_rows) &&
-           make_map_bf16(&p.tmHidden, at<uint16_t>(ws, L.hidden), T, H, GEMM_BK, a_rows) &&
+           make_map_bf16(&p.tmHidden, at<uint16_t>(ws, L.hidden), L.rows, H, GEMM_BK, a_rows) &&
            make_map_bf16(&p.tmB, W, V, H, GEMM_BK, 128);
 }
 
@@ -324,6 +326,7 @@ int moe_vocab_loss(int32_t T, int32_t H, int32_t V, const moe_bf16 *hidden, cons
     rp.status = status;
     rp.hidden = hidden;
     rp.packed = at<uint16_t>(ws, L.hidden);
+    rp.packed_rows = L.rows;
     rp.H = H;
     rp.loss = loss;
     rp.lse_out = lse;
@@ -333,7 +336,6 @@ int moe_vocab_loss(int32_t T, int32_t H, int32_t V, const moe_bf16 *hidden, cons
     memset(&p, 0, sizeof(p));
     if (!vocab_logits_maps(p, L, T, H, V, hidden, W_vocab, ws, few ? PAIR_FEW_ROWS : 128))
         return MOE_ERR_CUDA;
-    p.T = T;
     p.meta = meta;
     p.m_from_rows = 1;
     p.N = V;
@@ -395,6 +397,7 @@ int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hid
     rp.status = status;
     rp.hidden = hidden;
     rp.packed = at<uint16_t>(ws, L.hidden);
+    rp.packed_rows = L.rows;
     rp.H = H;
     rp.packed_of = at<int>(ws, L.packed_of);
     rp.dx_kblocks = L.piece / GEMM_BK;
@@ -406,30 +409,28 @@ int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hid
 
     uint16_t *dz = at<uint16_t>(ws, L.dz);
     float *part = at<float>(ws, L.part);
-    const int m_tiles = ceil_div(T, 256), h_tiles = ceil_div(H, 256);
+    const int m_tiles = ceil_div(L.rows, 256), h_tiles = ceil_div(H, 256);
     // z again, piece by piece, turned into dz in the epilogue
     PairGemmParams pz, px, pw;
     memset(&pz, 0, sizeof(pz));
     if (!vocab_logits_maps(pz, L, T, H, V, hidden, W_vocab, ws, 128) ||
-        !make_map_bf16(&pz.tmOut, dz, T, L.piece, 64, 32))
+        !make_map_bf16(&pz.tmOut, dz, L.rows, L.piece, 64, 32))
         return MOE_ERR_CUDA;
-    pz.T = T;
     pz.meta = meta;
     pz.m_from_rows = 1;
     pz.kblocks = pz.part_blocks = ceil_div(H, GEMM_BK);
     pz.splits = 1;
     pz.group_m = vocab_group(H);
-    pz.out_rows = T;
+    pz.out_rows = L.rows;
     pz.target = rp.packed_target;
     pz.lse = rp.packed_lse;
     pz.weight = rp.packed_weight;
     pz.status = status;
     // d_hidden partial sums [splits][rows, H] += dz W
     memset(&px, 0, sizeof(px));
-    if (!make_map_bf16(&px.tmA, dz, T, L.piece, GEMM_BK, 128) || !make_map_bf16(&px.tmB, W_vocab, V, H, 64, GEMM_BK) ||
+    if (!make_map_bf16(&px.tmA, dz, L.rows, L.piece, GEMM_BK, 128) || !make_map_bf16(&px.tmB, W_vocab, V, H, 64, GEMM_BK) ||
         !make_map_f32(&px.tmOut, part, L.part_rows, H, 32, 32))
         return MOE_ERR_CUDA;
-    px.T = T;
     px.meta = meta;
     px.m_from_rows = 1;
     px.N = H;
@@ -440,14 +441,13 @@ int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hid
     px.status = status;
     // dW piece = dz^T hidden
     memset(&pw, 0, sizeof(pw));
-    if (!make_map_bf16(&pw.tmA, dz, T, L.piece, 64, GEMM_BK) || !make_map_bf16(&pw.tmB, hidden, T, H, 64, GEMM_BK) ||
-        !make_map_bf16(&pw.tmHidden, at<uint16_t>(ws, L.hidden), T, H, 64, GEMM_BK) ||
+    if (!make_map_bf16(&pw.tmA, dz, L.rows, L.piece, 64, GEMM_BK) || !make_map_bf16(&pw.tmB, hidden, T, H, 64, GEMM_BK) ||
+        !make_map_bf16(&pw.tmHidden, at<uint16_t>(ws, L.hidden), L.rows, H, 64, GEMM_BK) ||
         !make_map_bf16(&pw.tmOut, dW_vocab, V, H, 64, 32))
         return MOE_ERR_CUDA;
-    pw.T = T;
     pw.meta = meta;
     pw.k_from_rows = 1;
-    pw.part_blocks = ceil_div(T, GEMM_BK);
+    pw.part_blocks = ceil_div(L.rows, GEMM_BK);
     pw.N = H;
     pw.splits = 1;
     pw.group_m = 1;

@@ -392,10 +392,20 @@ inline int choose_splits(int tiles, int kblocks, long long elements, int max_spl
 
 // What the vocabulary operators' row kernel leaves for the kernels after it.
 struct VocabMeta {
-    int rows;      // rows that count (target in [0, V) and not ignored)
+    int rows;      // rows of the products: those that count (target in [0, V) and not
+                   // ignored), and again as many where dz is written in two parts
+    int counted;   // rows that count: from here on they repeat, for the low parts
+    int packed;    // the products read the packed copies of the hidden rows
     float scale;   // backward: largest |d_loss| of them (1 when that is not finite)
     int splits;    // backward: K splits of the d_hidden product over those rows
 };
+// Backward: up to this many rows that count, dz is written in two bf16 parts,
+// the second as further rows: the products' tiles of 256 rows and the weight's one
+// K block of 64 have room for them.  Error of the gradients (2-norm; the result's own
+// rounding 1.66e-3) and time with one part and two: 4 rows 1.80e-3 (up to 3.5e-3 for
+// one row) 57.6 us, 1.66e-3 65.8; 31 rows 2.20e-3 75.7, 1.64e-3 81.2; 100 rows 2.21e-3
+// 134, 1.66e-3 150, where the roundings of dz average out and stay below 2.3e-3.
+constexpr int VOCAB_TWICE_ROWS = 32;
 constexpr int VOCAB_MAX_SPLITS = 16, VOCAB_MIN_SPLIT_BLOCKS = 8;
 
 // Two products of which neither reads or writes what the other writes: the
@@ -407,9 +417,8 @@ enum PairBeside { PG_ALONE = 0, PG_FIRST = 1, PG_SECOND = 2 };
 struct PairGemmParams {
     CUtensorMap tmA, tmB, tmOut;
     // the rows that count, packed: replaces A (STATS, DLOGITS) or B (BF16) when
-    // they are fewer than T; BF16_ADD: the addend, boxes of 64 columns x 32 rows
+    // meta->packed; BF16_ADD: the addend, boxes of 64 columns x 32 rows
     CUtensorMap tmHidden;
-    int T;                    // rows of `hidden`
     const VocabMeta *meta;    // NULL: M and kblocks as given
     int m_from_rows;          // M = meta->rows
     int k_from_rows;          // K = meta->rows
@@ -454,7 +463,8 @@ struct VocabRowsParams {
     int *packed_target;
     int *status;
     const uint16_t *hidden;   // [T, H]
-    uint16_t *packed;         // the counting rows' copies where some row does not count
+    uint16_t *packed;         // the counting rows' copies where some row does not count, or rows repeat
+    int packed_rows;          // rows that the packed arrays have room for
     int H;
     int dx_kblocks;           // backward: K blocks of the d_hidden product (of a vocabulary piece)
     float *loss, *lse_out;    // forward: zeroed where a row does not count

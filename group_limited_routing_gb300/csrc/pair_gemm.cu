@@ -233,7 +233,10 @@ __device__ __forceinline__ void epilogue_stats(const PairGemmParams &p, const Sh
 // dz of the warp's columns in bf16, 64 at a time.  The rounding (half a step,
 // 2^-8 of each value) makes dz an operand of the tensor core; the rows' weights
 // are divided by the largest of them first, so that a mean's equal weights
-// are 1 exactly and add no rounding of their own, common to every value.
+// are 1 exactly and add no rounding of their own, common to every value.  A few
+// rows' gradient is mostly that of their targets, whose roundings (of p - 1) do not
+// average out; there the rows repeat (VocabMeta) and the second time give what the
+// first rounding left.
 __device__ __forceinline__ void epilogue_dlogits(const PairGemmParams &p, const Shape &sh, const Unit &t,
                                                  uint32_t tacc, int half, int row, int row0, int lane, uint8_t *box)
 {
@@ -241,6 +244,7 @@ __device__ __forceinline__ void epilogue_dlogits(const PairGemmParams &p, const 
     const float nl = valid ? -p.lse[row] * LOG2E : 0.0f;
     const float w = valid ? p.weight[row] : 0.0f;
     const int target = valid ? p.target[row] - p.n0 : -1;
+    const bool low = valid && row >= p.meta->counted, any_low = __any_sync(0xffffffffu, low);
 #pragma unroll 1
     for (int c = t.n0 + half * PG_HALF; c < min(t.n0 + (half + 1) * PG_HALF, p.N); c += 64) {
         uint32_t r[64];
@@ -269,6 +273,15 @@ __device__ __forceinline__ void epilogue_dlogits(const PairGemmParams &p, const 
         for (int q = 0; q < 8; ++q)
             v[q] = make_uint4(bf16x2(f[8 * q], f[8 * q + 1]), bf16x2(f[8 * q + 2], f[8 * q + 3]),
                               bf16x2(f[8 * q + 4], f[8 * q + 5]), bf16x2(f[8 * q + 6], f[8 * q + 7]));
+        if (any_low) {
+            auto rest = [&](uint32_t hi, float a, float b) {
+                return low ? bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u)) : hi;
+            };
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                v[q] = make_uint4(rest(v[q].x, f[8 * q], f[8 * q + 1]), rest(v[q].y, f[8 * q + 2], f[8 * q + 3]),
+                                  rest(v[q].z, f[8 * q + 4], f[8 * q + 5]), rest(v[q].w, f[8 * q + 6], f[8 * q + 7]));
+        }
         store_box<false>(p, box, v, lane, c, row0);
     }
 }
@@ -389,7 +402,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
     const int npairs = (int)gridDim.x / 2;
     const int pair = (int)blockIdx.x / 2;
     const Shape sh = shape_of(p);
-    const bool packed = p.meta && p.meta->rows < p.T;
+    const bool packed = p.meta && p.meta->packed;
     const unsigned long long limit = p.wait_limit_ns ? p.wait_limit_ns : WAIT_LIMIT_NS;
     bool aborted_peer_loads = false;
 

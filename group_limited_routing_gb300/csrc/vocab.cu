@@ -88,16 +88,21 @@ __global__ void __launch_bounds__(ROWS_THREADS) vocab_rows_kernel(const VocabRow
     }
     const int total = n;
     const float scale = top > 0.0f && top < INFINITY ? top : 1.0f;
+    const bool twice = p.packed_of && total <= VOCAB_TWICE_ROWS;
+    const int rows = twice ? 2 * total : total;
+    const bool packed = twice || total < p.T;
     if (blockIdx.x == 0 && w == 0) {
         if (lane == 0) {
-            p.meta->rows = total;
+            p.meta->rows = rows;
+            p.meta->counted = total;
+            p.meta->packed = packed;
             p.meta->scale = scale;
         }
         if (p.packed_of) {
             // choose_splits, a candidate per lane
-            const int c = lane + 1, tiles = (total + 255) / 256 * ((p.H + 255) / 256);
+            const int c = lane + 1, tiles = (rows + 255) / 256 * ((p.H + 255) / 256);
             const bool may = c <= VOCAB_MAX_SPLITS && may_split(tiles, p.dx_kblocks, c, VOCAB_MIN_SPLIT_BLOCKS);
-            long long key = may ? split_cost(tiles, p.dx_kblocks, (long long)total * p.H, c) * 64 + c
+            long long key = may ? split_cost(tiles, p.dx_kblocks, (long long)rows * p.H, c) * 64 + c
                                 : 0x7fffffffffffffffll;
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1)
@@ -137,13 +142,18 @@ __global__ void __launch_bounds__(ROWS_THREADS) vocab_rows_kernel(const VocabRow
             if (p.d_loss) {
                 p.packed_lse[q] = p.lse[t];
                 p.packed_weight[q] = p.d_loss[t] / scale;
+                if (twice) {
+                    p.packed_target[total + q] = (int)v;
+                    p.packed_lse[total + q] = p.lse[t];
+                    p.packed_weight[total + q] = p.d_loss[t] / scale;
+                }
             }
         } else if (t < t1 && p.loss) {
             p.loss[t] = 0.0f;
             p.lse_out[t] = 0.0f;
         }
         __syncthreads();
-        if (total < p.T)
+        if (packed)
             for (int i = w; i < here; i += 32) {
                 const size_t from = (size_t)list[i] * nv, to = (size_t)(before + i) * nv;
                 for (int v0 = lane; v0 < nv; v0 += 8 * 32) {
@@ -156,12 +166,17 @@ __global__ void __launch_bounds__(ROWS_THREADS) vocab_rows_kernel(const VocabRow
                     for (int j = 0; j < 8; ++j)
                         if (v0 + 32 * j < nv)
                             dst[to + v0 + 32 * j] = q8[j];
+                    if (twice)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (v0 + 32 * j < nv)
+                                dst[to + (size_t)total * nv + v0 + 32 * j] = q8[j];
                 }
             }
         before += here;
     }
-    if (total < p.T)
-        for (int q = total + blockIdx.x; q < min(p.T, (total + 63) / 64 * 64); q += blocks)
+    if (packed)
+        for (int q = rows + blockIdx.x; q < min(p.packed_rows, (rows + 63) / 64 * 64); q += blocks)
             for (int v = threadIdx.x; v < nv; v += ROWS_THREADS)
                 dst[(size_t)q * nv + v] = make_uint4(0, 0, 0, 0);
 }
@@ -182,7 +197,7 @@ __global__ void __launch_bounds__(1024) vocab_join_kernel(const float2 *__restri
     pdl_wait();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int r = threadIdx.x % R, part = threadIdx.x / R;
-    const int rows = meta->rows;
+    const int rows = meta->rows;               // (forward: rows that count)
     const bool in = (int)blockIdx.x * R + r < rows;
     auto join = [](float2 a, float2 b) {
         const float top = fmaxf(a.x, b.x);
@@ -222,13 +237,14 @@ __global__ void __launch_bounds__(1024) vocab_join_kernel(const float2 *__restri
 }
 
 // d_hidden[t] = bf16( scale sum_s part[s][packed row of t] ), zero where the
-// row does not count.  Splits in order.
+// row does not count.  Splits in order; a low part's sums after the high part's.
 __global__ void __launch_bounds__(128) vocab_dx_join_kernel(const float *__restrict__ part, const VocabMeta *meta,
                                                             const int *packed_of, int T, int H, uint16_t *d_hidden)
 {
     pdl_wait();
     const float scale = meta->scale;
     const int splits = meta->splits;
+    const int counted = meta->counted, twice = meta->rows > counted;
     const size_t split_stride = (size_t)((meta->rows + 255) / 256 * 256) * H;
     const int nv = H / 8;
     for (int t = blockIdx.x; t < T; t += gridDim.x) {
@@ -236,8 +252,10 @@ __global__ void __launch_bounds__(128) vocab_dx_join_kernel(const float *__restr
         for (int v = threadIdx.x; v < nv; v += blockDim.x) {
             float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (r >= 0)
-                for (int s = 0; s < splits; ++s) {
-                    const float4 *q = reinterpret_cast<const float4 *>(part + s * split_stride + (size_t)r * H) + 2 * v;
+                for (int s = 0; s < splits << twice; ++s) {
+                    const bool low = s >= splits;
+                    const size_t at = (low ? s - splits : s) * split_stride + (size_t)(low ? r + counted : r) * H;
+                    const float4 *q = reinterpret_cast<const float4 *>(part + at) + 2 * v;
                     const float4 a = __ldcs(q), b = __ldcs(q + 1);
                     f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
                     f[4] += b.x; f[5] += b.y; f[6] += b.z; f[7] += b.w;

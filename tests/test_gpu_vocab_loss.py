@@ -178,6 +178,36 @@ def test_infinite_and_nan_logits_show_in_their_rows_only():
     assert torch.equal(loss[keep], base[keep]) and torch.isfinite(clean).all()
 
 
+@pytest.mark.parametrize("T,H,V,keep", [(1, 64, 300, 1), (3, 1000, 5000, 3), (16, 512, 1111, 16), (17, 72, 600, 17),
+                                        (31, 1544, 3000, 31), (32, 256, 2000, 32), (33, 256, 2000, 32),
+                                        (40, 128, 700, 9), (150, 128, 700, 0), (1000, 264, 900, 31)])
+def test_few_rows_gradient_keeps_its_digits(T, H, V, keep):
+    """Up to 32 rows that count, dz is two bf16 parts: what is left out of it is
+    half a step of half a step, 2^-16, so that only the result's rounding, 2^-8,
+    is of bf16's size."""
+    d = inputs(T, H, V, seed=T + V)
+    off = torch.randperm(T, generator=torch.Generator().manual_seed(T))[keep:]
+    d["target"][off.to(DEV)] = IGN
+    _, lse, g, status = run(d)
+    assert status == 0
+    k = keep_of(d)
+    if keep == 0:
+        return                      # (check_backward: zeros)
+    z, zb = logits(d)
+    z, zb, l = z[k], zb[k], lse[k].double()[:, None]
+    h, W, t = d["hidden"][k].double(), d["W"].double(), d["target"][k].long()[:, None]
+    p = (z - l).exp()
+    w = d["d_loss"][k].double()[:, None]
+    dz = w * (p - torch.zeros_like(p).scatter_(1, t, 1.0))
+    err = dz.abs() * (2.0 ** -16 + 4 * U) + w * p * (zb + U * (8 + 4 * z.abs() + 4 * l.abs()))
+    steps = 2 * U * (max(p.shape) / 16 + 24)
+    for name, ref, bound in (("d_hidden", dz @ W, err @ W.abs() + steps * (dz.abs() @ W.abs())),
+                             ("dW_vocab", dz.t() @ h, err.t() @ h.abs() + steps * (dz.abs().t() @ h.abs()))):
+        out = (g[name][k] if name == "d_hidden" else g[name]).double()
+        over = ((out - ref).abs() / (bound + 2.0 ** -8 * ref.abs() + 1e-37)).max().item()
+        assert over <= 1, "%s off by %.3g of its bound" % (name, over)
+
+
 def test_several_vocabulary_pieces():
     """dz of the whole vocabulary would pass the workspace's piece."""
     d = inputs(4096, 64, 140001, ignored=0.02, seed=8)
