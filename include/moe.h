@@ -452,7 +452,8 @@ int moe_vocab_loss(int32_t T, int32_t H, int32_t V, const moe_bf16 *hidden, cons
  *   dW_vocab [V, H] bf16 out = dz^T hidden, overwritten
  * The logits are formed again, a piece of the vocabulary at a time; dz is
  * rounded to bf16 as an operand of the two products (relative to the largest
- * |d_loss|), whose sums are fp32 and rounded once.  Workspace of
+ * |d_loss|; up to 32 rows that count: as two bf16 parts), whose sums are fp32
+ * and rounded once.  Workspace of
  * moe_vocab_loss_workspace_bytes(T, H, V, 1) bytes: dz of one piece (1 GiB at
  * most, or 256 columns of it) and fp32 sums of d_hidden.  Deterministic. */
 int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hidden, const moe_bf16 *W_vocab,
