@@ -97,6 +97,7 @@ class TrainStack:
         x, saved = self._saved
         head = self.head.backward(d_loss)
         d_n, d_r = head["d_hidden"], None
+        d_y = d_n                          # (nobody else has it; the layers' d_hidden are handed back)
         out = dict(dW_vocab=head["dW_vocab"], dw_pre=torch.empty_like(self.w_pre), dw_post=torch.empty_like(self.w_post),
                    d_gate=torch.empty_like(self.gate), layers=[None] * len(self.layers))
         for i in reversed(range(len(self.layers))):
@@ -104,10 +105,10 @@ class TrainStack:
             g = moe.block_norm_backward(r, y, self.gate[i], self.w_post[i], self.w_pre[i + 1], d_r, d_n,
                                         alpha=self.alpha, eps=self.eps, ws=self.ws_norm,
                                         out=dict(dw_pre=out["dw_pre"][i + 1], dw_post=out["dw_post"][i],
-                                                 d_gate=out["d_gate"][i], d_y=d_n, **({} if d_r is None else {"d_x": d_r})))
+                                                 d_gate=out["d_gate"][i], d_y=d_y, **({} if d_r is None else {"d_x": d_r})))
             d_r = g["d_x"]
             layer = self.layers[i]
-            e = layer.backward(g["d_y"])
+            e = layer.backward(d_y)
             rb = moe.route_backward(self.cfg, layer._hidden, layer.W_router, layer.routing[0], e["d_topk_w"],
                                     d_aux_loss=d_aux_loss, expert_counts=None if d_aux_loss is None else layer.routing[2],
                                     d_hidden_add=e["d_hidden"], W_split=layer.W_split, ws=self.ws_route,
