@@ -705,7 +705,10 @@ class MoELayer:
     aux=True also returns the balance loss (not with the fused router).  The
     router weight is split once at construction (prepare_router); call
     prepare() again after changing W_router in place.  Layers of a stack may
-    share one workspace (ws_layer, or ws_route / ws_fwd for the two calls)."""
+    share one workspace (ws_layer, or ws_route / ws_fwd for the two calls).
+
+    `routing` is the last call's; calls write it to the same tensors each time,
+    or to those given to the call (new_routing()), which no other call touches."""
 
     def __init__(self, cfg: MoeConfig, W_router, expert_bias, W_gate_up, W_down, shared_gate_up, shared_down,
                  aux: bool = False, ws_route: Optional[Workspace] = None, ws_fwd: Optional[Workspace] = None,
@@ -729,6 +732,7 @@ class MoELayer:
             self.ws_route = ws_route or Workspace(cfg, _lib.MOE_WS_ROUTE, self.device)
             self.ws_fwd = ws_fwd or Workspace(cfg, _lib.MOE_WS_FORWARD, self.device)
         self.routing = None
+        self._own_routing = None        # (kept: a captured call holds their addresses)
         self.last_launches = 0
         self.W_split = None
         self.prepare()
@@ -737,18 +741,33 @@ class MoELayer:
         """(Re)make the bf16 x 3 split of W_router that routing reads."""
         self.W_split = prepare_router(self.cfg, self.W_router, out=self.W_split)
 
-    def __call__(self, hidden, residual=None, out=None):
+    def new_routing(self):
+        """Tensors for one call's routing: (topk_idx, topk_w, expert_counts), with
+        aux (.., aux_P, aux_loss)."""
+        cfg, dev = self.cfg, self.device
+        f32, i32 = torch.float32, torch.int32
+        r = (torch.empty(cfg.T, cfg.k, dtype=i32, device=dev), torch.empty(cfg.T, cfg.k, dtype=f32, device=dev),
+             torch.empty(cfg.E, dtype=i32, device=dev))
+        if self.aux:
+            return r + (torch.empty(cfg.E, dtype=f32, device=dev), torch.empty(1, dtype=f32, device=dev))
+        return r if self.single_call else r + (None, None)
+
+    def __call__(self, hidden, residual=None, out=None, routing=None):
+        if routing is None:
+            if self._own_routing is None or len(self._own_routing) != (5 if self.aux or not self.single_call else 3):
+                self._own_routing = self.new_routing()
+            routing = self._own_routing
         self._hidden = hidden
         if self.single_call:
             y, self.routing = layer(self.cfg, hidden, self.W_router, self.expert_bias, self.W_gate_up, self.W_down,
                                     self.shared_gate_up, self.shared_down, residual, W_split=self.W_split,
-                                    flags=self.flags, ws=self.ws_layer, out=out, routing=self.routing, aux=self.aux)
+                                    flags=self.flags, ws=self.ws_layer, out=out, routing=routing, aux=self.aux)
             self.last_launches = last_launch_count()
             return y
         self.routing = route(self.cfg, hidden, self.W_router, self.expert_bias, aux=self.aux, ws=self.ws_route,
-                             out=self.routing, W_split=self.W_split)
+                             out=routing, W_split=self.W_split)
         n = last_launch_count()
-        idx, w = self.routing[0], self.routing[1]
+        idx, w = routing[0], routing[1]
         y = forward(self.cfg, hidden, self.W_gate_up, self.W_down, self.shared_gate_up, self.shared_down, idx,
                     w, residual, ws=self.ws_fwd, out=out)
         self.last_launches = n + last_launch_count()
@@ -763,16 +782,18 @@ class MoELayer:
             st |= self.ws_bwd.status()
         return st
 
-    def backward(self, d_out, out: Optional[dict] = None) -> dict:
+    def backward(self, d_out, out: Optional[dict] = None, call=None) -> dict:
         """Gradients of the last call's output w.r.t. its input, the expert
         weights and the routing weights, for that call's routing (moe_backward;
-        the router's own gradient and the residual path are not included)."""
-        if self.routing is None:
+        the router's own gradient and the residual path are not included), or of
+        an earlier call: `call` = (its hidden, the routing tensors it was given)."""
+        if call is None and self.routing is None:
             raise RuntimeError("backward() needs a forward call first")
+        hidden, routing = (self._hidden, self.routing) if call is None else call
         if getattr(self, "ws_bwd", None) is None:
             self.ws_bwd = Workspace(self.cfg, _lib.MOE_WS_BACKWARD, self.device)
-        g = backward(self.cfg, self._hidden, self.W_gate_up, self.W_down, self.shared_gate_up, self.shared_down,
-                     self.routing[0], self.routing[1], d_out, ws=self.ws_bwd, out=out)
+        g = backward(self.cfg, hidden, self.W_gate_up, self.W_down, self.shared_gate_up, self.shared_down,
+                     routing[0], routing[1], d_out, ws=self.ws_bwd, out=out)
         self.last_launches = last_launch_count()
         return g
 

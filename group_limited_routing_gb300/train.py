@@ -9,7 +9,10 @@ Layer l of L computes, with n_0 = RMS(x) w_pre[0],
     y_l = layer_l(n_l)
     r_{l+1}, n_{l+1} = block_norm(r_l, y_l, gate[l], w_post[l], w_pre[l + 1])
 and the head's loss is that of n_L.  Everything runs in the library's kernels
-on the current stream; this module only passes tensors between them.
+on the current stream; this module only passes tensors between them.  A backward
+reads the tensors of its own forward call (x, target and the weights must still
+hold what they held then), so layers and head may be called by others in between
+and a layer may stand in several places.
 """
 from __future__ import annotations
 
@@ -23,7 +26,7 @@ from . import moe
 class VocabHead:
     """The vocabulary's weight [V, H] bf16 and the workspaces of its loss:
     __call__(hidden, target) is vocab_loss, backward(d_loss) the gradient of the
-    last call."""
+    last call, or of an earlier one whose (hidden, target, lse) it is given."""
 
     def __init__(self, W_vocab, T: int, ignore_index: int = -100):
         V, H = W_vocab.shape
@@ -39,13 +42,14 @@ class VocabHead:
         self._last = (hidden, target, lse)
         return loss, lse
 
-    def backward(self, d_loss, out: Optional[dict] = None) -> dict:
+    def backward(self, d_loss, out: Optional[dict] = None, call=None) -> dict:
         """dict(d_hidden [T, H] bf16, dW_vocab [V, H] bf16)."""
-        if self._last is None:
+        call = call or self._last
+        if call is None:
             raise RuntimeError("backward() needs a forward call first")
         if self.ws_bwd is None:
             self.ws_bwd = moe.vocab_loss_workspace(*self._shape, backward=True, device=self.device)
-        hidden, target, lse = self._last
+        hidden, target, lse = call
         return moe.vocab_loss_backward(hidden, self.W_vocab, target, lse, d_loss, ignore_index=self.ignore_index,
                                        ws=self.ws_bwd, out=out)
 
@@ -55,7 +59,7 @@ class VocabHead:
 
 class TrainStack:
     """layers: MoELayer objects of one configuration (aux=True adds the balance
-    loss); w_pre [L + 1, H], w_post [L, H] and gate [L, H] or [L, groups, H] fp32;
+    loss; one object may stand in several places); w_pre [L + 1, H], w_post [L, H] and gate [L, H] or [L, groups, H] fp32;
     alpha the residual scale."""
 
     def __init__(self, layers, head: VocabHead, w_pre, w_post, gate, alpha: float = 1.0, eps: float = 1e-6):
@@ -76,41 +80,47 @@ class TrainStack:
         r, n = moe.block_norm(x, w_pre=self.w_pre[0], eps=self.eps)
         saved = []
         for i, layer in enumerate(self.layers):
-            y = layer(n)
-            saved.append((r, y))
+            call = (n, layer.new_routing())
+            y = layer(n, routing=call[1])
+            saved.append((r, y, call))
             r, n = moe.block_norm(r, y, self.gate[i], self.w_post[i], self.w_pre[i + 1], alpha=self.alpha,
                                   eps=self.eps)
-        self._saved = (x, saved)
-        return self.head(n, target)
+        loss, lse = self.head(n, target)
+        self._saved = (x, saved, (n, target, lse))
+        return loss, lse
 
     def aux_loss(self):
         """The last call's balance losses, one per layer ([1] fp32 each)."""
-        return [layer.routing[4] for layer in self.layers]
+        if self._saved is None:
+            raise RuntimeError("aux_loss() needs a forward call first")
+        return [call[1][4] for _, _, call in self._saved[1]]
 
     def backward(self, d_loss, d_aux_loss=None) -> dict:
         """Gradients of the last call for d_loss [T] fp32 (and d_aux_loss [1] fp32,
         the weight of every layer's balance loss): dict(d_x, dW_vocab, dw_pre
-        [L + 1, H], dw_post [L, H], d_gate [L, groups, H], layers: per layer what
-        moe.backward gives with d_hidden replaced by the whole one, and dW_router)."""
+        [L + 1, H], dw_post [L, H], d_gate [L, groups, H], layers: per place in
+        the stack what moe.backward gives with d_hidden replaced by the whole one,
+        and dW_router)."""
         if self._saved is None:
             raise RuntimeError("backward() needs a forward call first")
-        x, saved = self._saved
-        head = self.head.backward(d_loss)
+        x, saved, head_call = self._saved
+        head = self.head.backward(d_loss, call=head_call)
         d_n, d_r = head["d_hidden"], None
         d_y = d_n                          # (nobody else has it; the layers' d_hidden are handed back)
         out = dict(dW_vocab=head["dW_vocab"], dw_pre=torch.empty_like(self.w_pre), dw_post=torch.empty_like(self.w_post),
                    d_gate=torch.empty_like(self.gate), layers=[None] * len(self.layers))
         for i in reversed(range(len(self.layers))):
-            r, y = saved[i]
+            r, y, call = saved[i]
+            hidden, routing = call
             g = moe.block_norm_backward(r, y, self.gate[i], self.w_post[i], self.w_pre[i + 1], d_r, d_n,
                                         alpha=self.alpha, eps=self.eps, ws=self.ws_norm,
                                         out=dict(dw_pre=out["dw_pre"][i + 1], dw_post=out["dw_post"][i],
                                                  d_gate=out["d_gate"][i], d_y=d_y, **({} if d_r is None else {"d_x": d_r})))
             d_r = g["d_x"]
             layer = self.layers[i]
-            e = layer.backward(d_y)
-            rb = moe.route_backward(self.cfg, layer._hidden, layer.W_router, layer.routing[0], e["d_topk_w"],
-                                    d_aux_loss=d_aux_loss, expert_counts=None if d_aux_loss is None else layer.routing[2],
+            e = layer.backward(d_y, call=call)
+            rb = moe.route_backward(self.cfg, hidden, layer.W_router, routing[0], e["d_topk_w"],
+                                    d_aux_loss=d_aux_loss, expert_counts=None if d_aux_loss is None else routing[2],
                                     d_hidden_add=e["d_hidden"], W_split=layer.W_split, ws=self.ws_route,
                                     out=dict(d_hidden=e["d_hidden"]))
             e["dW_router"] = rb["dW_router"]

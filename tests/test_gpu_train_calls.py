@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+from group_limited_routing_gb300 import moe, train
 from test_gpu_train import DEV, build, near
 
 pytestmark = pytest.mark.gpu
@@ -57,3 +58,98 @@ def test_every_layers_d_hidden(stream):
         near(g["layers"][i]["d_hidden"], want, "layer %d d_hidden" % i)
     tensors = [t for e in g["layers"] for t in e.values()] + [v for k, v in g.items() if k != "layers"]
     assert len({t.data_ptr() for t in tensors}) == len(tensors)      # nothing handed back shares memory
+
+
+def twin(layer):
+    """Another layer object over the same weights."""
+    return moe.MoELayer(layer.cfg, layer.W_router, layer.expert_bias, layer.W_gate_up, layer.W_down,
+                        layer.shared_gate_up, layer.shared_down, aux=layer.aux, single_call=layer.single_call)
+
+
+def flat(g):
+    return [g[k] for k in ("d_x", "dW_vocab", "dw_pre", "dw_post", "d_gate")] + \
+        [e[k] for e in g["layers"] for k in sorted(e)]
+
+
+def same(a, b):
+    return len(a) == len(b) and all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("single_call", [True, False])
+def test_one_layer_at_two_places(single_call):
+    """A layer object that stands twice gives the bits of two objects over the
+    same weights."""
+    step, x, target = build(L=3, seed=6)
+    a, b = step.layers[:2]
+    if not single_call:
+        a.single_call = b.single_call = False
+        a, b = twin(a), twin(b)
+    rest = (step.head, step.w_pre, step.w_post, step.gate)
+    one, two = (train.TrainStack(layers, *rest, alpha=0.9) for layers in ([a, b, a], [a, b, twin(a)]))
+    d_loss, d_aux = torch.full((96,), 1.0 / 96, device=DEV), torch.tensor([0.02], device=DEV)
+    want_loss = two(x, target)
+    want_aux = [t.clone() for t in two.aux_loss()]
+    want = flat(two.backward(d_loss, d_aux))
+    assert same(one(x, target), want_loss)
+    assert same(one.aux_loss(), want_aux)
+    assert not torch.equal(want_aux[0], want_aux[2])
+    assert same(flat(one.backward(d_loss, d_aux)), want)
+
+
+def test_calls_between_a_forward_and_its_backward():
+    """Layers and head called on other data, alone and in another stack, before the
+    first stack's backward: its gradients are those of its own call, and so are
+    the other stack's."""
+    step, x, target = build(L=2, seed=7)
+    _, x2, target2 = build(L=2, seed=8)
+    d_loss, d_aux = torch.full((96,), 1.0 / 96, device=DEV), torch.tensor([0.02], device=DEV)
+    other = train.TrainStack(step.layers, step.head, step.w_pre, step.w_post, step.gate, alpha=0.9)
+    losses, wants, auxes = [], [], []
+    for a, t in ((x, target), (x2, target2)):
+        losses.append(step(a, t))
+        auxes.append([v.clone() for v in step.aux_loss()])
+        wants.append(flat(step.backward(d_loss, d_aux)))
+    step(x, target)
+    other(x2, target2)
+    n = moe.rmsnorm(x2.bfloat16())
+    for layer in step.layers:
+        layer(n)
+        layer(n.flip(0).contiguous())
+    step.head(n, target2)
+    assert same(step.aux_loss(), auxes[0]) and same(other.aux_loss(), auxes[1])
+    assert same(flat(step.backward(d_loss, d_aux)), wants[0])
+    assert same(flat(other.backward(d_loss, d_aux)), wants[1])
+    assert same(flat(step.backward(d_loss, d_aux)), wants[0])        # and again
+
+
+def test_a_captured_layer_keeps_its_routing_tensors():
+    """A graph of a layer's call writes the tensors that it was captured with: a
+    step in between neither frees them nor has its own overwritten by a replay."""
+    step, x, target = build(L=1, seed=9)
+    layer = step.layers[0]
+    d_loss = torch.full((96,), 1.0 / 96, device=DEV)
+    step(x, target)
+    want = flat(step.backward(d_loss))
+    n = moe.rmsnorm(torch.randn(96, 512, device=DEV).bfloat16())
+    eager = layer(n).clone()
+    graph = moe.GraphedStep(layer, n)
+    mine = layer.routing
+    step(x, target)
+    assert all(a.data_ptr() != b.data_ptr() for a, b in zip(layer.routing, mine))
+    assert torch.equal(graph(n), eager)
+    torch.cuda.synchronize()
+    assert same(flat(step.backward(d_loss)), want)
+    layer(n)
+    assert all(a.data_ptr() == b.data_ptr() for a, b in zip(layer.routing, mine))
+
+
+def test_feedback_after_a_step():
+    """layer.routing is the last call's, a step's too: expert_feedback follows it."""
+    step, x, target = build(L=1, seed=10)
+    layer = step.layers[0]
+    layer(moe.rmsnorm(x.flip(0).contiguous()))
+    step(x, target)
+    totals = torch.zeros(layer.cfg.E, dtype=torch.int64, device=DEV)
+    layer.feedback(0.001, totals)
+    counts = torch.bincount(step.layers[0].routing[0].flatten().long(), minlength=layer.cfg.E)
+    assert torch.equal(totals, counts)
