@@ -493,9 +493,15 @@ def _sized(ws: Optional[SizedWorkspace], need: int, what: str, device) -> Option
     return SizedWorkspace(need, what, device) if ws is None and need else ws
 
 
+def block_norm_workspace_bytes(T: int, H: int, groups: int = 1) -> int:
+    """moe_block_norm_workspace_bytes (0: the shape is not supported).  Fewer groups
+    may need more: each has its own plan."""
+    return int(_lib.load().moe_block_norm_workspace_bytes(T, H, groups))
+
+
 def block_norm_workspace(T: int, H: int, groups: int = 1, device=None) -> SizedWorkspace:
-    """The workspace of block_norm_backward."""
-    return SizedWorkspace(_lib.load().moe_block_norm_workspace_bytes(T, H, groups), "moe_block_norm_backward", device)
+    """The workspace of block_norm_backward (groups: rows of its gate, 1 without)."""
+    return SizedWorkspace(block_norm_workspace_bytes(T, H, groups), "moe_block_norm_backward", device)
 
 
 def _block_norm_args(x, y, gate, w_post, w_pre):

@@ -71,7 +71,11 @@ class TrainStack:
         self.cfg = self.layers[0].cfg
         self.device = self.layers[0].device
         self.ws_route = moe.route_backward_workspace(self.cfg, self.device)
-        self.ws_norm = moe.block_norm_workspace(self.cfg.T, self.cfg.H, self.gate.shape[1], self.device)
+        # the norms behind the layers and the one in front of the first, which has no
+        # gate: its plan is that of one group, whose partial sums may be more
+        size = moe.block_norm_workspace_bytes
+        self.ws_norm = moe.SizedWorkspace(max(size(self.cfg.T, self.cfg.H, self.gate.shape[1]),
+                                              size(self.cfg.T, self.cfg.H)), "moe_block_norm_backward", self.device)
         self._saved = None
 
     def __call__(self, x, target):

@@ -419,7 +419,8 @@ int moe_block_norm(int32_t T, int32_t H, int32_t groups, int32_t stream_f32, con
  *   d_gate [groups, H], dw_post [H], dw_pre [H] fp32 out, overwritten; each may
  *          be NULL (with gate, w_post or w_pre NULL they are the gradients at 1)
  * x and y are the forward's inputs; nothing else is kept from it.  Workspace of
- * moe_block_norm_workspace_bytes(T, H, groups) bytes.  Deterministic. */
+ * moe_block_norm_workspace_bytes(T, H, groups) bytes, groups 1 without a gate (one
+ * plan per shape: fewer groups may need more).  Deterministic. */
 size_t moe_block_norm_workspace_bytes(int32_t T, int32_t H, int32_t groups);
 int moe_block_norm_backward(int32_t T, int32_t H, int32_t groups, int32_t stream_f32, const void *x,
                             const moe_bf16 *y, const float *gate, const float *w_post, const float *w_pre,

@@ -153,3 +153,15 @@ def test_feedback_after_a_step():
     layer.feedback(0.001, totals)
     counts = torch.bincount(step.layers[0].routing[0].flatten().long(), minlength=layer.cfg.E)
     assert torch.equal(totals, counts)
+
+
+def test_first_norm_of_a_stack_with_several_gates():
+    """Three gate rows at a size where the norm without a gate needs more workspace
+    than those with; the last step is that norm's gradient, bit for bit."""
+    step, x, target = build(T=3000, H=512, I=256, L=1, V=300, groups=3, seed=2, stream=torch.float32)
+    step(x, target)
+    g = step.backward(torch.full((3000,), 1.0 / 3000, device=DEV))
+    assert step.status() == 0
+    size = moe._lib.load().moe_block_norm_workspace_bytes
+    assert size(3000, 512, 1) > size(3000, 512, 3)
+    assert g["d_x"].shape == x.shape and g["d_x"].isfinite().all() and g["dw_pre"].isfinite().all()
