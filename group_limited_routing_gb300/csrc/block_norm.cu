@@ -635,8 +635,10 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const BlockNor
             float q5[5] = {sum2(t[0]), sum2(t[1]), sum2(t[2]), sum2(t[3]), sum2(t[4])};
             block_sums5(q5, sm5, slot5);
             const float sigma = rsqrtf(q5[0] * inv_h + p.eps);
-            // dr = d_r + sigma dq - (sigma^3 mean(dq r)) r
-            const float c_r = sigma * sigma * sigma * (q5[1] * inv_h);
+            // dr = d_r + sigma dq - c_r r, c_r = sigma^2 mean(dq q) = sigma (sigma (sigma mean(dq r))):
+            // from the inside each factor stays near the gradient's size, while sigma^3 leaves
+            // fp32's range from RMS(r) = 1e-13 down, where sigma^2 is at 1e26
+            const float c_r = sigma * (sigma * (sigma * (q5[1] * inv_h)));
             const float c_u = (q5[2] + sigma * q5[3] - c_r * q5[4]) * inv_h;   // mean(du u)
             const F2 sigma2 = f2(sigma), ncr = f2(-c_r), ncu = f2(-c_u);
 #pragma unroll
