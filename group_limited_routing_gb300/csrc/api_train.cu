@@ -63,10 +63,11 @@ cudaError_t pair_product(PairEpilogue epi, PairProduct product, PairGemmParams p
 // 8.2e-7, 2.42 ms; three 5.3e-7, 2.45 ms; four 4.0e-7, 2.49 ms; an fp32 matrix
 // product 4.7e-7.
 constexpr int LOGIT_PART_BLOCKS = 11;
-// At most this many rows, whose few losses average nothing out, take shorter
-// parts: T = 3, H = 3144, V = 87989 1.3e-6 -> 5e-7 at worst (an fp32 product,
+// At most this many rows that count (of however many; the device knows) take
+// shorter parts: T = 3, H = 3144, V = 87989 1.3e-6 -> 5e-7 at worst (an fp32 product,
 // there a sum per element, 3e-7), for a quarter more time (T = 16, H = 2048, V =
-// 131072: 96 -> 119 us, which is why more rows keep the longer ones).
+// 131072: 96 -> 119 us).  That price is why more rows keep the longer parts, whose
+// errors, as large row by row, partly cancel in a sum over the rows.
 constexpr int LOGIT_EXACT_ROWS = 8, LOGIT_EXACT_BLOCKS = 4;
 
 // ---------------------------------------------------------- vocabulary loss
@@ -340,8 +341,9 @@ int moe_vocab_loss(int32_t T, int32_t H, int32_t V, const moe_bf16 *hidden, cons
     p.m_from_rows = 1;
     p.N = V;
     p.kblocks = ceil_div(H, GEMM_BK);
-    p.part_blocks = ceil_div(p.kblocks, ceil_div(p.kblocks, T <= LOGIT_EXACT_ROWS ? LOGIT_EXACT_BLOCKS
-                                                                                  : LOGIT_PART_BLOCKS));
+    p.part_blocks = ceil_div(p.kblocks, ceil_div(p.kblocks, LOGIT_PART_BLOCKS));
+    p.few_rows = LOGIT_EXACT_ROWS;
+    p.few_part_blocks = ceil_div(p.kblocks, ceil_div(p.kblocks, LOGIT_EXACT_BLOCKS));
     p.splits = 1;
     p.group_m = vocab_group(H);
     p.target = rp.packed_target;

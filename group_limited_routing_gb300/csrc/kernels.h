@@ -427,6 +427,7 @@ struct PairGemmParams {
     int a_off[3], b_off[3];   // rows added to the operand's row coordinate (of each part)
     int splits;               // K range cut among this many units; 0: meta->splits
     int part_blocks;          // K blocks per accumulator (STATS, PARTIAL; else at least kblocks)
+    int few_part_blocks, few_rows;   // (not 0:) the same while meta->rows <= few_rows
     int beside;               // PairBeside
     int group_m;              // tiles run m-fastest within groups of this many m-tiles
     int out_row0;             // row of the output map where row 0 goes

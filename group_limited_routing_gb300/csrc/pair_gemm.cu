@@ -113,7 +113,7 @@ struct Unit {
 };
 
 struct Shape {
-    int M, m_tiles, n_tiles, kblocks, splits, split_rows, units;
+    int M, m_tiles, n_tiles, kblocks, part_blocks, splits, split_rows, units;
 };
 
 __device__ __forceinline__ Shape shape_of(const PairGemmParams &p)
@@ -122,6 +122,7 @@ __device__ __forceinline__ Shape shape_of(const PairGemmParams &p)
     const int rows = p.meta ? p.meta->rows : 0;
     sh.M = p.m_from_rows ? rows : p.M;
     sh.kblocks = p.k_from_rows ? (rows + GEMM_BK - 1) / GEMM_BK : p.kblocks;
+    sh.part_blocks = p.few_part_blocks && rows <= p.few_rows ? p.few_part_blocks : p.part_blocks;
     sh.m_tiles = (sh.M + PG_BM - 1) / PG_BM;
     sh.n_tiles = (p.N + PG_BN - 1) / PG_BN;
     sh.splits = p.splits ? p.splits : p.meta->splits;
@@ -144,7 +145,7 @@ __device__ __forceinline__ Unit unit_of(const PairGemmParams &p, const Shape &sh
     t.n0 = t.nt * PG_BN;
     t.k0 = (int)((long long)sh.kblocks * t.split / sh.splits);
     t.k1 = (int)((long long)sh.kblocks * (t.split + 1) / sh.splits);
-    t.parts = (t.k1 - t.k0 + p.part_blocks - 1) / p.part_blocks;
+    t.parts = (t.k1 - t.k0 + sh.part_blocks - 1) / sh.part_blocks;
     return t;
 }
 
@@ -485,7 +486,7 @@ __global__ void __launch_bounds__(PG_THREADS, 1) pair_gemm_kernel(const __grid_c
             for (int u = pair; ok && u < sh.units; u += npairs) {
                 const Unit t = unit_of(p, sh, u);
                 for (int part = 0; ok && part < t.parts; ++part) {
-                    const int kp = t.k0 + part * p.part_blocks, ke = min(kp + p.part_blocks, t.k1);
+                    const int kp = t.k0 + part * sh.part_blocks, ke = min(kp + sh.part_blocks, t.k1);
                     const uint32_t slot = ctr % PG_SLOTS, par = (ctr / PG_SLOTS) & 1u;
                     // (the peer's epilogue warps arrive here across the pair)
                     if (!mbar_wait_cluster(tempty0 + 8u * slot, par ^ 1u, abort_flag, limit)) {
