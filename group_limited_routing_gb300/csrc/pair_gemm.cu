@@ -35,6 +35,8 @@
 // MOE_STATUS_TIMEOUT.
 #include <cuda_bf16.h>
 
+#include <float.h>
+
 #include <algorithm>
 
 #include "kernels.h"
@@ -189,8 +191,10 @@ __device__ __forceinline__ void store_box(const PairGemmParams &p, uint8_t *box,
 }
 
 // Softmax statistics of this lane's row over the warp's 128 columns: a base b
-// (in log2) and s = sum 2^(z log2 e - b).  b is finite even when the largest
-// logit is not, so that an infinite or NaN logit shows in s.
+// (in log2) and s = sum 2^(z log2 e - b).  The exponentials' base is finite even
+// when the largest logit is not, so that an infinite or NaN logit shows in s.  With
+// +inf it is the largest fp32, which no other block's base exceeds when the blocks are
+// joined; columns of -inf alone leave the join's neutral element (-inf, 0).
 __device__ __forceinline__ void epilogue_stats(const PairGemmParams &p, const Shape &sh, const Unit &t,
                                                uint32_t (&z)[PG_HALF], int half, int row)
 {
@@ -207,13 +211,15 @@ __device__ __forceinline__ void epilogue_stats(const PairGemmParams &p, const Sh
 #pragma unroll
     for (int i = 0; i < PG_HALF; ++i)
         m[i & 3] = fmaxf(m[i & 3], __uint_as_float(z[i]));
-    float base = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * LOG2E;
-    if (!(fabsf(base) < INFINITY))
-        base = 0.0f;
+    const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * LOG2E;
+    float base = top > -INFINITY ? fminf(top, FLT_MAX) : 0.0f;
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < PG_HALF; ++i)
         s[i & 3] += ex2_approx(fmaf(__uint_as_float(z[i]), LOG2E, -base));
+    const float sum = (s[0] + s[1]) + (s[2] + s[3]);
+    if (!(top > -INFINITY) && sum == 0.0f)          // (a NaN among them is in the sum)
+        base = -INFINITY;
     const bool valid = row < sh.M;
     const int at = valid ? p.target[row] - (p.n0 + col0) : -1;
     const bool mine = at >= 0 && at < ncols;
@@ -225,7 +231,7 @@ __device__ __forceinline__ void epilogue_stats(const PairGemmParams &p, const Sh
                 zt = __uint_as_float(z[i]);
     }
     if (valid) {
-        p.stats[(size_t)(2 * t.nt + half) * p.ld_stats + row] = make_float2(base, (s[0] + s[1]) + (s[2] + s[3]));
+        p.stats[(size_t)(2 * t.nt + half) * p.ld_stats + row] = make_float2(base, sum);
         if (mine)
             p.target_logit[row] = zt;
     }
