@@ -114,7 +114,8 @@ VocabLayout vocab_layout(int T, int H, int V, bool backward)
         L.weight = take(4ull * L.rows);
         const size_t most = std::max<size_t>(1, VOCAB_PIECE_BYTES / (512ull * L.rows));   // 256-column blocks
         L.piece = (int)std::min<size_t>(L.ntiles, most) * 256;
-        L.dz = take(2ull * L.rows * L.piece);
+        // (never less than fewer rows' piece takes, which may fill its bytes better)
+        L.dz = take(std::min(512ull * L.rows * L.ntiles, std::max<unsigned long long>(VOCAB_PIECE_BYTES, 512ull * L.rows)));
         // fp32 sums of d_hidden: one slice per split, and as few rows as count
         // (which the host does not know) may be split the most
         const int h_tiles = ceil_div(H, 256), m_tiles = ceil_div(L.rows, 256);

@@ -24,9 +24,9 @@ from . import moe
 
 
 class VocabHead:
-    """The vocabulary's weight [V, H] bf16 and the workspaces of its loss:
-    __call__(hidden, target) is vocab_loss, backward(d_loss) the gradient of the
-    last call, or of an earlier one whose (hidden, target, lse) it is given."""
+    """The vocabulary's weight [V, H] bf16 and the workspaces of its loss over T rows
+    at most: __call__(hidden, target) is vocab_loss, backward(d_loss) the gradient of
+    the last call, or of an earlier one whose (hidden, target, lse) it is given."""
 
     def __init__(self, W_vocab, T: int, ignore_index: int = -100):
         V, H = W_vocab.shape

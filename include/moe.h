@@ -439,8 +439,8 @@ int moe_block_norm_backward(int32_t T, int32_t H, int32_t groups, int32_t stream
  *   target   [T] int32 or int64 (target_bits 32 or 64)
  *   loss, lse [T] fp32 out
  * Products of bf16 in fp32 on the tensor cores; the softmax in fp32.
- * Workspace of moe_vocab_loss_workspace_bytes(T, H, V, 0) bytes.
- * Deterministic. */
+ * Workspace of moe_vocab_loss_workspace_bytes(T, H, V, 0) bytes (one sized for
+ * more rows serves fewer).  Deterministic. */
 size_t moe_vocab_loss_workspace_bytes(int32_t T, int32_t H, int32_t V, int backward);
 int moe_vocab_loss(int32_t T, int32_t H, int32_t V, const moe_bf16 *hidden, const moe_bf16 *W_vocab,
                    const void *target, int32_t target_bits, int64_t ignore_index, float *loss, float *lse, void *ws,
@@ -456,7 +456,8 @@ int moe_vocab_loss(int32_t T, int32_t H, int32_t V, const moe_bf16 *hidden, cons
  * |d_loss|; up to 32 rows that count: as two bf16 parts), whose sums are fp32
  * and rounded once.  Workspace of
  * moe_vocab_loss_workspace_bytes(T, H, V, 1) bytes: dz of one piece (1 GiB at
- * most, or 256 columns of it) and fp32 sums of d_hidden.  Deterministic. */
+ * most, or 256 columns of it) and fp32 sums of d_hidden; one sized for more rows
+ * serves fewer.  Deterministic. */
 int moe_vocab_loss_backward(int32_t T, int32_t H, int32_t V, const moe_bf16 *hidden, const moe_bf16 *W_vocab,
                             const void *target, int32_t target_bits, int64_t ignore_index, const float *lse,
                             const float *d_loss, moe_bf16 *d_hidden, moe_bf16 *dW_vocab, void *ws, size_t ws_bytes,
