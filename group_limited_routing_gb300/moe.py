@@ -38,13 +38,21 @@ class MoeConfig:
     eps: float = 1e-20
 
     def c(self) -> _lib.MoeCfg:
-        # (made once: the library takes it by const pointer, and the fields never change)
-        c = self.__dict__.get("_c")
-        if c is None:
-            c = _lib.MoeCfg(self.T, self.H, self.E, self.n_group, self.topk_group, self.k, self.I, self.Is, self.rsf,
-                            self.eps)
-            object.__setattr__(self, "_c", c)
-        return c
+        """A new structure of these fields, the caller's own."""
+        return _lib.MoeCfg(self.T, self.H, self.E, self.n_group, self.topk_group, self.k, self.I, self.Is, self.rsf,
+                           self.eps)
+
+    def ref(self):
+        """A pointer for the library's calls, which take it as const (made once per
+        configuration: the fields never change)."""
+        r = self.__dict__.get("_ref")
+        if r is None:
+            r = ctypes.byref(self.c())
+            object.__setattr__(self, "_ref", r)
+        return r
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
 
     def with_T(self, T: int) -> "MoeConfig":
         return dataclasses.replace(self, T=T)
@@ -56,9 +64,9 @@ WS_LAYER = 3
 
 def workspace_bytes(cfg: MoeConfig, which: int, flags: int = 0) -> int:
     if which == WS_LAYER:
-        n = _lib.load().moe_layer_workspace_bytes(ctypes.byref(cfg.c()), flags)
+        n = _lib.load().moe_layer_workspace_bytes(cfg.ref(), flags)
     else:
-        n = _lib.load().moe_workspace_bytes(ctypes.byref(cfg.c()), which)
+        n = _lib.load().moe_workspace_bytes(cfg.ref(), which)
     if n == 0:
         raise ValueError("configuration not supported: %r" % (cfg,))
     return int(n)
@@ -138,7 +146,7 @@ def prepare_router(cfg: MoeConfig, W_router, out=None):
     pw = _need(W_router, "W_router", torch.float32, (cfg.E, cfg.H), dev)
     W_split = out if out is not None else torch.empty(3, cfg.E, cfg.H, dtype=torch.bfloat16, device=dev)
     ps = _need(W_split, "W_split", torch.bfloat16, (3, cfg.E, cfg.H), dev)
-    _lib.check(_lib.load().moe_prepare_router(ctypes.byref(cfg.c()), pw, ps, _stream(dev)), "moe_prepare_router")
+    _lib.check(_lib.load().moe_prepare_router(cfg.ref(), pw, ps, _stream(dev)), "moe_prepare_router")
     return W_split
 
 
@@ -165,11 +173,11 @@ def route(cfg: MoeConfig, hidden, W_router, expert_bias=None, *, aux: bool = Fal
     pL = None if aux_loss is None else aux_loss.data_ptr()
     lib = _lib.load()
     if ps is None:
-        rc = lib.moe_route(ctypes.byref(cfg.c()), ph, pw, pb, idx.data_ptr(), w.data_ptr(), counts.data_ptr(),
+        rc = lib.moe_route(cfg.ref(), ph, pw, pb, idx.data_ptr(), w.data_ptr(), counts.data_ptr(),
                            pP, pL, ws.ptr, ws.nbytes, _stream(dev))
         _lib.check(rc, "moe_route")
     else:
-        rc = lib.moe_route_prepared(ctypes.byref(cfg.c()), ph, pw, ps, pb, idx.data_ptr(), w.data_ptr(),
+        rc = lib.moe_route_prepared(cfg.ref(), ph, pw, ps, pb, idx.data_ptr(), w.data_ptr(),
                                     counts.data_ptr(), pP, pL, ws.ptr, ws.nbytes, _stream(dev))
         _lib.check(rc, "moe_route_prepared")
     return idx, w, counts, aux_P, aux_loss
@@ -182,7 +190,7 @@ def router_logits(cfg: MoeConfig, hidden, W_router, *, ws: Optional[Workspace] =
     pw = _need(W_router, "W_router", torch.float32, (cfg.E, cfg.H), dev)
     logits = torch.empty(cfg.T, cfg.E, dtype=torch.float32, device=dev)
     ws = _ws(ws, cfg, _lib.MOE_WS_ROUTE, dev)
-    _lib.check(_lib.load().moe_router_logits(ctypes.byref(cfg.c()), ph, pw, logits.data_ptr(), ws.ptr, ws.nbytes,
+    _lib.check(_lib.load().moe_router_logits(cfg.ref(), ph, pw, logits.data_ptr(), ws.ptr, ws.nbytes,
                                              _stream(dev)), "moe_router_logits")
     return logits
 
@@ -210,7 +218,7 @@ def route_from_logits(cfg: MoeConfig, logits, expert_bias=None, *, aux: bool = F
     aux_P = torch.empty(cfg.E, dtype=torch.float32, device=dev) if aux else None
     aux_loss = torch.empty(1, dtype=torch.float32, device=dev) if aux else None
     ws = _ws(ws, cfg, _lib.MOE_WS_ROUTE, dev)
-    rc = _lib.load().moe_route_from_logits(ctypes.byref(cfg.c()), pl, pb, idx.data_ptr(), w.data_ptr(),
+    rc = _lib.load().moe_route_from_logits(cfg.ref(), pl, pb, idx.data_ptr(), w.data_ptr(),
                                            counts.data_ptr(), None if aux_P is None else aux_P.data_ptr(),
                                            None if aux_loss is None else aux_loss.data_ptr(), ws.ptr, ws.nbytes,
                                            _stream(dev))
@@ -235,7 +243,7 @@ def forward(cfg: MoeConfig, hidden, W_gate_up, W_down, shared_gate_up, shared_do
         out = torch.empty(cfg.T, cfg.H, dtype=bf, device=dev)
     po = _need(out, "out", bf, (cfg.T, cfg.H), dev)
     ws = _ws(ws, cfg, _lib.MOE_WS_FORWARD, dev)
-    rc = _lib.load().moe_forward(ctypes.byref(cfg.c()), ph, pgu, pd, psgu, psd, pi, pw, pr, po, ws.ptr, ws.nbytes,
+    rc = _lib.load().moe_forward(cfg.ref(), ph, pgu, pd, psgu, psd, pi, pw, pr, po, ws.ptr, ws.nbytes,
                                  _stream(dev))
     _lib.check(rc, "moe_forward")
     return out
@@ -281,7 +289,7 @@ def layer(cfg: MoeConfig, hidden, W_router, expert_bias, W_gate_up, W_down, shar
         ws = Workspace(cfg, WS_LAYER, dev, flags)
     elif ws.which != WS_LAYER or not ws.fits(cfg, flags):
         raise ValueError("workspace of the wrong kind or too small")
-    rc = _lib.load().moe_layer(ctypes.byref(cfg.c()), ph, pwr, psp, pb, pgu, pd, psgu, psd, pr, pi, pw, pc, pP, pl,
+    rc = _lib.load().moe_layer(cfg.ref(), ph, pwr, psp, pb, pgu, pd, psgu, psd, pr, pi, pw, pc, pP, pl,
                                po, flags, ws.ptr, ws.nbytes, _stream(dev))
     _lib.check(rc, "moe_layer")
     return out, routing
@@ -315,7 +323,7 @@ def backward(cfg: MoeConfig, hidden, W_gate_up, W_down, shared_gate_up, shared_d
         _need(t, name, dt, shape, dev)
         g[name] = t
     ws = _ws(ws, cfg, _lib.MOE_WS_BACKWARD, dev)
-    rc = _lib.load().moe_backward(ctypes.byref(cfg.c()), ph, pgu, pd, psgu, psd, pi, pw, pdo,
+    rc = _lib.load().moe_backward(cfg.ref(), ph, pgu, pd, psgu, psd, pi, pw, pdo,
                                   g["d_hidden"].data_ptr(), g["dW_gate_up"].data_ptr(), g["dW_down"].data_ptr(),
                                   g["d_shared_gate_up"].data_ptr(), g["d_shared_down"].data_ptr(),
                                   g["d_topk_w"].data_ptr(), ws.ptr, ws.nbytes, _stream(dev))
@@ -393,12 +401,12 @@ class SizedWorkspace:
 
 def ep_dispatch_workspace_bytes(cfg: MoeConfig, ranks: int) -> int:
     """moe_ep_dispatch_workspace_bytes (0: the shape is not supported)."""
-    return int(_lib.load().moe_ep_dispatch_workspace_bytes(ctypes.byref(cfg.c()), ranks))
+    return int(_lib.load().moe_ep_dispatch_workspace_bytes(cfg.ref(), ranks))
 
 
 def expert_rows_workspace_bytes(cfg: MoeConfig, rows: int) -> int:
     """moe_expert_rows_workspace_bytes (0: the shape is not supported)."""
-    return int(_lib.load().moe_expert_rows_workspace_bytes(ctypes.byref(cfg.c()), rows))
+    return int(_lib.load().moe_expert_rows_workspace_bytes(cfg.ref(), rows))
 
 
 def ep_dispatch(cfg: MoeConfig, ranks: int, hidden, topk_idx, *, ws: Optional[SizedWorkspace] = None):
@@ -413,11 +421,11 @@ def ep_dispatch(cfg: MoeConfig, ranks: int, hidden, topk_idx, *, ws: Optional[Si
     x_send = torch.empty(n, cfg.H, dtype=torch.bfloat16, device=dev)
     e_send = torch.empty(n, dtype=torch.int32, device=dev)
     slot_of = torch.empty(cfg.T, cfg.k, dtype=torch.int32, device=dev)
-    need = int(_lib.load().moe_ep_dispatch_workspace_bytes(ctypes.byref(cfg.c()), ranks))
+    need = int(_lib.load().moe_ep_dispatch_workspace_bytes(cfg.ref(), ranks))
     if need and (ws is None or ws.nbytes < need):
         ws = SizedWorkspace(need, "moe_ep_dispatch", dev)
     # (an unsupported shape has no workspace size: the call itself names the error)
-    rc = _lib.load().moe_ep_dispatch(ctypes.byref(cfg.c()), ranks, ph, pi, counts.data_ptr(), x_send.data_ptr(),
+    rc = _lib.load().moe_ep_dispatch(cfg.ref(), ranks, ph, pi, counts.data_ptr(), x_send.data_ptr(),
                                      e_send.data_ptr(), slot_of.data_ptr(), ws.ptr if need else None,
                                      ws.nbytes if need else 0, _stream(dev))
     _lib.check(rc, "moe_ep_dispatch")
@@ -438,10 +446,10 @@ def expert_rows(cfg: MoeConfig, x, expert, W_gate_up, W_down, *, ws: Optional[Si
     po = _need(out, "out", torch.bfloat16, (rows, cfg.H), dev)
     if rows == 0:
         return out
-    need = int(_lib.load().moe_expert_rows_workspace_bytes(ctypes.byref(cfg.c()), rows))
+    need = int(_lib.load().moe_expert_rows_workspace_bytes(cfg.ref(), rows))
     if need and (ws is None or ws.nbytes < need):
         ws = SizedWorkspace(need, "moe_expert_rows", dev)
-    rc = _lib.load().moe_expert_rows(ctypes.byref(cfg.c()), rows, px, pe, pgu, pd, po, ws.ptr if need else None,
+    rc = _lib.load().moe_expert_rows(cfg.ref(), rows, px, pe, pgu, pd, po, ws.ptr if need else None,
                                      ws.nbytes if need else 0, _stream(dev))
     _lib.check(rc, "moe_expert_rows")
     return out
@@ -458,7 +466,7 @@ def combine(cfg: MoeConfig, Y, shared_row0: int, slot_of, topk_w, residual=None,
     if out is None:
         out = torch.empty(cfg.T, cfg.H, dtype=torch.bfloat16, device=dev)
     po = _need(out, "out", torch.bfloat16, (cfg.T, cfg.H), dev)
-    rc = _lib.load().moe_combine(ctypes.byref(cfg.c()), py, rows, shared_row0, ps, pw, pr, po, _stream(dev))
+    rc = _lib.load().moe_combine(cfg.ref(), py, rows, shared_row0, ps, pw, pr, po, _stream(dev))
     _lib.check(rc, "moe_combine")
     return out
 
@@ -470,7 +478,7 @@ def expert_feedback(cfg: MoeConfig, counts, gamma: float, expert_bias=None, tota
     pc = _need(counts, "expert_counts", torch.int32, (cfg.E,), dev)
     pb = _opt(expert_bias, "expert_bias", torch.float32, (cfg.E,), dev)
     pt = _opt(totals, "totals", torch.int64, (cfg.E,), dev)
-    _lib.check(_lib.load().moe_expert_feedback(ctypes.byref(cfg.c()), pc, gamma, pb, pt, _stream(dev)),
+    _lib.check(_lib.load().moe_expert_feedback(cfg.ref(), pc, gamma, pb, pt, _stream(dev)),
                "moe_expert_feedback")
 
 
@@ -639,7 +647,7 @@ def vocab_loss_backward(hidden, W_vocab, target, lse, d_loss, *, ignore_index: i
 
 def route_backward_workspace(cfg: MoeConfig, device=None) -> SizedWorkspace:
     """The workspace of route_backward."""
-    return SizedWorkspace(_lib.load().moe_route_backward_workspace_bytes(ctypes.byref(cfg.c())),
+    return SizedWorkspace(_lib.load().moe_route_backward_workspace_bytes(cfg.ref()),
                           "moe_route_backward", device)
 
 
@@ -668,9 +676,9 @@ def route_backward(cfg: MoeConfig, hidden, W_router, topk_idx, d_topk_w, *, d_au
             t = torch.empty(*shape, dtype=dt, device=dev)
         _need(t, name, dt, shape, dev)
         g[name] = t
-    need = int(_lib.load().moe_route_backward_workspace_bytes(ctypes.byref(cfg.c())))
+    need = int(_lib.load().moe_route_backward_workspace_bytes(cfg.ref()))
     ws = _sized(ws, need, "moe_route_backward", dev)
-    rc = _lib.load().moe_route_backward(ctypes.byref(cfg.c()), ph, pw, ps, pi, pd, pc, pa, pp,
+    rc = _lib.load().moe_route_backward(cfg.ref(), ph, pw, ps, pi, pd, pc, pa, pp,
                                         g["d_hidden"].data_ptr(), g["dW_router"].data_ptr(),
                                         ws.ptr if need else None, ws.nbytes if need else 0, _stream(dev))
     _lib.check(rc, "moe_route_backward")
