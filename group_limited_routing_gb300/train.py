@@ -59,23 +59,36 @@ class VocabHead:
 
 class TrainStack:
     """layers: MoELayer objects of one configuration (aux=True adds the balance
-    loss; one object may stand in several places); w_pre [L + 1, H], w_post [L, H] and gate [L, H] or [L, groups, H] fp32;
-    alpha the residual scale."""
+    loss; one object may stand in several places); w_pre [L + 1, H], w_post [L, H]
+    and gate [L, H] or [L, groups, H] fp32; alpha the residual scale."""
 
     def __init__(self, layers, head: VocabHead, w_pre, w_post, gate, alpha: float = 1.0, eps: float = 1e-6):
         self.layers = list(layers)
+        if not self.layers:
+            raise ValueError("a stack needs a layer")
+        self.cfg = self.layers[0].cfg
+        self.device = self.layers[0].device
+        for layer in self.layers:
+            if layer.cfg != self.cfg:
+                raise ValueError("layers of one configuration expected, got %r and %r" % (self.cfg, layer.cfg))
+        L, H = len(self.layers), self.cfg.H
+        for name, t, shape in (("w_pre", w_pre, (L + 1, H)), ("w_post", w_post, (L, H))):
+            if tuple(t.shape) != shape:
+                raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+        groups = gate.shape[1] if gate.dim() == 3 else 1
+        if tuple(gate.shape) not in ((L, H), (L, groups, H)) or groups < 1 or self.cfg.T % groups:
+            raise ValueError("gate must have shape %s or (%d, groups, %d), groups dividing T = %d, got %s" %
+                             ((L, H), L, H, self.cfg.T, tuple(gate.shape)))
         self.head = head
         self.w_pre, self.w_post = w_pre, w_post
         self.gate = gate if gate.dim() == 3 else gate[:, None, :]
         self.alpha, self.eps = alpha, eps
-        self.cfg = self.layers[0].cfg
-        self.device = self.layers[0].device
         self.ws_route = moe.route_backward_workspace(self.cfg, self.device)
         # the norms behind the layers and the one in front of the first, which has no
         # gate: its plan is that of one group, whose partial sums may be more
         size = moe.block_norm_workspace_bytes
-        self.ws_norm = moe.SizedWorkspace(max(size(self.cfg.T, self.cfg.H, self.gate.shape[1]),
-                                              size(self.cfg.T, self.cfg.H)), "moe_block_norm_backward", self.device)
+        self.ws_norm = moe.SizedWorkspace(max(size(self.cfg.T, H, groups), size(self.cfg.T, H)),
+                                          "moe_block_norm_backward", self.device)
         self._saved = None
 
     def __call__(self, x, target):
