@@ -46,8 +46,10 @@ EXPORTS = ("moe_workspace_bytes", "moe_workspace_init", "moe_route", "moe_router
 MOE_ROUTE_STATIC_SCRATCH_BYTES = 40 << 20
 MOE_LAYER_FUSED_ROUTER = 1
 MOE_LAYER_FUSED_COMBINE = 2
-MOE_KERNEL_COUNT = 30
-MOE_KERNEL_STAGE_ROUTE_PERMUTE = 29   # moe_profile_read id of the routing + bucketing stage (mode 2)
+MOE_KERNEL_COUNT = 19
+MOE_KERNEL_TRAIN_FIRST = 32
+MOE_KERNEL_TRAIN_COUNT = 11
+MOE_KERNEL_STAGE_ROUTE_PERMUTE = 18   # moe_profile_read id of the routing + bucketing stage (mode 2)
 
 
 class MoeCfg(ctypes.Structure):

@@ -25,22 +25,33 @@ namespace {
 thread_local int g_last_launches = 0;
 
 // ------------------------------------------------------------- profiling
-const char *const kKernelNames[MOE_KERNEL_COUNT] = {
+const char *const kLayerKernelNames[MOE_KERNEL_COUNT] = {
     "split_router", "router_gemm", "route_select", "route_finalize", "bucket_hist",
     "bucket_scan", "bucket_scatter", "gemm_gate_up_swiglu", "gemm_down", "combine", "dense_tiles",
     "bwd_gate_up_recompute", "bwd_dgrad_down_swiglu", "bwd_dgrad_x", "bwd_weight_grads", "bwd_pad_and_dw",
-    "router_route_bucket", "bucket_tiles",
+    "router_route_bucket", "bucket_tiles", "router_plus_permute"};
+const char *const kTrainKernelNames[MOE_KERNEL_TRAIN_COUNT] = {
     "block_norm", "block_norm_backward", "vocab_rows", "vocab_logits", "vocab_join", "vocab_dlogits",
     "vocab_d_hidden", "vocab_d_weight", "route_backward_scores", "route_backward_d_hidden",
-    "route_backward_d_weight", "router_plus_permute"};
+    "route_backward_d_weight"};
+
+// the name of a kernel id, NULL where there is no such id
+const char *kernel_name(int id)
+{
+    if (id >= 0 && id < MOE_KERNEL_COUNT)
+        return kLayerKernelNames[id];
+    if (id >= MOE_KERNEL_TRAIN_FIRST && id < MOE_KERNEL_TRAIN_FIRST + MOE_KERNEL_TRAIN_COUNT)
+        return kTrainKernelNames[id - MOE_KERNEL_TRAIN_FIRST];
+    return nullptr;
+}
 
 std::atomic<int> g_prof_on{0};
 std::atomic<int> g_inject_timeouts{0};   // test-only: GEMM launches left to sabotage
 std::mutex g_prof_mu;
 std::vector<ProfRecord> g_prof_pending;
 std::vector<cudaEvent_t> g_event_pool;
-double g_prof_ms[MOE_KERNEL_COUNT];
-long long g_prof_n[MOE_KERNEL_COUNT];
+double g_prof_ms[KID_END];
+long long g_prof_n[KID_END];
 
 cudaEvent_t pool_event()
 {
@@ -1464,7 +1475,7 @@ int moe_profile_enable(int on)
 
 int moe_profile_read(int kernel_id, double *total_ms, int32_t *launches, int reset)
 {
-    if (kernel_id < 0 || kernel_id >= MOE_KERNEL_COUNT || !total_ms || !launches)
+    if (!kernel_name(kernel_id) || !total_ms || !launches)
         return MOE_ERR_INVALID_ARG;
     std::lock_guard<std::mutex> g(g_prof_mu);
     int rc = MOE_OK;
@@ -1489,9 +1500,8 @@ int moe_profile_read(int kernel_id, double *total_ms, int32_t *launches, int res
 
 const char *moe_kernel_name(int kernel_id)
 {
-    if (kernel_id < 0 || kernel_id >= MOE_KERNEL_COUNT)
-        return "";
-    return kKernelNames[kernel_id];
+    const char *name = kernel_name(kernel_id);
+    return name ? name : "";
 }
 
 const char *moe_strerror(int code)

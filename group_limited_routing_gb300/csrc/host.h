@@ -17,10 +17,13 @@ enum KernelId {
     KID_SPLIT = 0, KID_ROUTER_GEMM, KID_SELECT, KID_FINALIZE, KID_HIST, KID_SCAN, KID_SCATTER,
     KID_GEMM_GATE_UP, KID_GEMM_DOWN, KID_COMBINE, KID_DENSE_TILES, KID_BWD_RECOMPUTE, KID_BWD_DGRAD,
     KID_BWD_DX, KID_BWD_WGRAD, KID_BWD_MISC, KID_ROUTE_FUSED, KID_TILES,
-    KID_BLOCK_NORM, KID_BLOCK_NORM_BWD, KID_VOCAB_ROWS, KID_VOCAB_LOGITS, KID_VOCAB_JOIN, KID_VOCAB_DLOGITS,
-    KID_VOCAB_DX, KID_VOCAB_DW, KID_ROUTE_BWD_SCORES, KID_ROUTE_BWD_DX, KID_ROUTE_BWD_DW,
-    KID_STAGE_ROUTE_PERMUTE   // (per-stage timing) the routing and bucketing kernels as one interval
+    KID_STAGE_ROUTE_PERMUTE,  // (per-stage timing) the routing and bucketing kernels as one interval
+    KID_BLOCK_NORM = MOE_KERNEL_TRAIN_FIRST, KID_BLOCK_NORM_BWD, KID_VOCAB_ROWS, KID_VOCAB_LOGITS, KID_VOCAB_JOIN, KID_VOCAB_DLOGITS,
+    KID_VOCAB_DX, KID_VOCAB_DW, KID_ROUTE_BWD_SCORES, KID_ROUTE_BWD_DX, KID_ROUTE_BWD_DW, KID_END
 };
+static_assert(KID_STAGE_ROUTE_PERMUTE == MOE_KERNEL_STAGE_ROUTE_PERMUTE &&
+              KID_STAGE_ROUTE_PERMUTE + 1 == MOE_KERNEL_COUNT &&
+              KID_END == MOE_KERNEL_TRAIN_FIRST + MOE_KERNEL_TRAIN_COUNT, "ids are part of the ABI");
 
 // whether a launch is to be sabotaged (moe_debug_inject_timeout); counts it
 bool take_injected_timeout();

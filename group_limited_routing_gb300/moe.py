@@ -701,7 +701,8 @@ def profile_read(reset: bool = True) -> dict:
     """{kernel name: (total ms, launches)} recorded since the last reset."""
     lib = _lib.load()
     out = {}
-    for kid in range(_lib.MOE_KERNEL_COUNT):
+    first = _lib.MOE_KERNEL_TRAIN_FIRST
+    for kid in [*range(_lib.MOE_KERNEL_COUNT), *range(first, first + _lib.MOE_KERNEL_TRAIN_COUNT)]:
         ms = ctypes.c_double(0.0)
         n = ctypes.c_int32(0)
         _lib.check(lib.moe_profile_read(kid, ctypes.byref(ms), ctypes.byref(n), 1 if reset else 0),

@@ -502,10 +502,14 @@ int moe_last_launch_count(void);
  * kernel on its own; events are recorded only where the stage changes.
  * moe_profile_enable(0) stops.  moe_profile_read() waits for the recorded
  * events, folds them into per-kernel totals and returns the total
- * milliseconds and interval count of `kernel_id` (0 <= kernel_id <
- * MOE_KERNEL_COUNT), clearing them when reset != 0. */
-#define MOE_KERNEL_COUNT 30
-#define MOE_KERNEL_STAGE_ROUTE_PERMUTE 29
+ * milliseconds and interval count of `kernel_id`, clearing them when reset != 0.
+ * Ids: 0 to MOE_KERNEL_COUNT - 1 for the layer's kernels, the last of them the
+ * stage, and MOE_KERNEL_TRAIN_FIRST to + MOE_KERNEL_TRAIN_COUNT - 1 for those of the
+ * training operators (moe_kernel_name() is empty for any other). */
+#define MOE_KERNEL_COUNT 19
+#define MOE_KERNEL_STAGE_ROUTE_PERMUTE 18
+#define MOE_KERNEL_TRAIN_FIRST 32
+#define MOE_KERNEL_TRAIN_COUNT 11
 int moe_profile_enable(int on);
 int moe_profile_read(int kernel_id, double *total_ms, int32_t *launches, int reset);
 const char *moe_kernel_name(int kernel_id);
