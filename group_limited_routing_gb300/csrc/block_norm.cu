@@ -36,8 +36,9 @@
 // Measured on one GB300 (copy rate 6.79 TB/s): T = 32768, H = 2048 in bf16
 // forward 92 us, 5.8 TB/s (0.86 of the copy rate); backward with the column sums
 // 150 us, 5.4 TB/s (0.79), its two reductions per row and their barriers being
-// the rest; T = 4095, H = 1536, fp32 stream, backward 39 us (0.43: five rows per
-// block do not outlast a block's start and the column sums' kernel).
+// the rest; with an fp32 stream 191 us (0.62) and 271 us (0.66; two rows in flight).
+// T = 4095, H = 1536, fp32 stream, backward 39 us (0.43: five rows per block do not
+// outlast a block's start and the column sums' kernel).
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -767,7 +768,9 @@ __global__ void __launch_bounds__(FIN_THREADS) block_norm_finish_kernel(const Bl
             p.dw_post[out] = post;
         return;
     }
-    // many groups: each by one slice
+    // many groups: each by one slice, a group's chunks in sequence.  T = 32768, H = 2048:
+    // 165 us with 8 groups, 159 with 16 and 64, against 152 with one; T = 65536, H = 256,
+    // where a group has the most chunks: 88 us with 8, 48 with 64, against 42 with one.
     float4 wp = make_float4(1.f, 1.f, 1.f, 1.f), post = zero;
     if (in && p.w_post)
         wp = *reinterpret_cast<const float4 *>(p.w_post + h);

@@ -401,10 +401,14 @@ struct VocabMeta {
 };
 // Backward: up to this many rows that count, dz is written in two bf16 parts,
 // the second as further rows: the products' tiles of 256 rows and the weight's one
-// K block of 64 have room for them.  Error of the gradients (2-norm; the result's own
-// rounding 1.66e-3) and time with one part and two: 4 rows 1.80e-3 (up to 3.5e-3 for
-// one row) 57.6 us, 1.66e-3 65.8; 31 rows 2.20e-3 75.7, 1.64e-3 81.2; 100 rows 2.21e-3
-// 134, 1.66e-3 150, where the roundings of dz average out and stay below 2.3e-3.
+// K block of 64 have room for them.  At H = 2048, V = 32768, the gradients' error
+// (2-norm, mean and worst of six inputs; the result's own rounding is 1.66e-3) and time
+// with one part and with two:
+//   4 rows    1.97e-3  2.50e-3  119 us      1.66e-3  1.90e-3  124 us
+//   31 rows   2.22e-3  2.37e-3  122 us      1.66e-3  1.70e-3  124 us
+//   100 rows  2.19e-3  2.22e-3  119 us      1.66e-3  1.67e-3  135 us
+// More rows keep one part: their worst case is their mean, and the second part then
+// costs its share of every product.
 constexpr int VOCAB_TWICE_ROWS = 32;
 constexpr int VOCAB_MAX_SPLITS = 16, VOCAB_MIN_SPLIT_BLOCKS = 8;
 

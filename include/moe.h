@@ -389,10 +389,9 @@ int moe_expert_feedback(const moe_cfg *cfg, const int32_t *expert_counts, float 
 int moe_rmsnorm(int32_t T, int32_t H, const moe_bf16 *x, moe_bf16 *out, float eps, void *stream);
 
 /* ---- Training operators ----------------------------------------------------
- * What a training step of a stack of these layers needs beside moe_backward:
- * the norms around a block, the loss over the vocabulary and the router's
- * gradient.  The pages train the model but print none of these; the formulas
- * below define them.
+ * What training needs beside moe_backward: the norms around a block, the loss over
+ * the vocabulary and the router's gradient.  The pages train the model but print
+ * none of these; the formulas below define them.
  *
  * Norms around a block, fused with the block's gate and the residual scale.
  * With RMS(z) = z / sqrt(mean_h z^2 + eps), x the residual stream, y the
@@ -407,7 +406,9 @@ int moe_rmsnorm(int32_t T, int32_t H, const moe_bf16 *x, moe_bf16 *out, float ep
  *   r      [T, H] out, x's type (may alias x; may be NULL when y is)
  *   n      [T, H] bf16 out (may alias y)
  * fp32 arithmetic, each output rounded once.  H % 8 == 0, H <= 8192,
- * T % groups == 0, pointers 16-byte aligned.  gate and w_post need y. */
+ * T % groups == 0, pointers 16-byte aligned.  gate and w_post need y.
+ * Pre-norm layers, x + layer(RMS(x)), take n from the call with y NULL and, in
+ * the backward, the gradient of the sum as d_r and that of n as d_n. */
 int moe_block_norm(int32_t T, int32_t H, int32_t groups, int32_t stream_f32, const void *x, const moe_bf16 *y,
                    const float *gate, const float *w_post, const float *w_pre, float alpha, float eps, void *r,
                    moe_bf16 *n, void *stream);
@@ -489,7 +490,8 @@ int moe_get_status(void *ws, size_t ws_bytes, void *stream, int32_t *status, int
 
 /* Number of kernels the last successful moe_route / moe_route_prepared /
  * moe_prepare_router / moe_forward / moe_layer / moe_route_from_logits /
- * moe_router_logits call on this thread enqueued (memsets not counted). */
+ * moe_router_logits call or training operator on this thread enqueued (memsets
+ * not counted). */
 int moe_last_launch_count(void);
 
 /* Kernel timing.  moe_profile_enable(1): every kernel the library launches
