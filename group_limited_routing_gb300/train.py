@@ -132,7 +132,7 @@ class TrainStack:
             g = moe.block_norm_backward(r, y, self.gate[i], self.w_post[i], self.w_pre[i + 1], d_r, d_n,
                                         alpha=self.alpha, eps=self.eps, ws=self.ws_norm,
                                         out=dict(dw_pre=out["dw_pre"][i + 1], dw_post=out["dw_post"][i],
-                                                 d_gate=out["d_gate"][i], d_y=d_y, **({} if d_r is None else {"d_x": d_r})))
+                                                 d_gate=out["d_gate"][i], d_y=d_y, d_x=d_r))
             d_r = g["d_x"]
             layer = self.layers[i]
             e = layer.backward(d_y, call=call)
