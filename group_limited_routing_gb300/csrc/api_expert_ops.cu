@@ -508,6 +508,7 @@ int moe_adamw(int32_t count, const moe_adamw_tensor *tensors, const moe_adamw_cf
     c.b2 = (float)cfg->beta2;
     c.one_b2 = (float)(1.0 - cfg->beta2);
     c.eps = (float)cfg->eps;
+    c.one = 1.0f;
     const double step = (double)std::max<int64_t>(cfg->step, 1);
     c.step_host = std::max<int64_t>(cfg->step, 1);
     c.size = (float)(cfg->lr / (1.0 - pow(cfg->beta1, step)));

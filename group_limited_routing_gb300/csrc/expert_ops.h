@@ -123,6 +123,7 @@ struct AdamScalars {
     double lr, beta1, beta2;
     float b1, one_b1, b2, one_b2, eps;
     float size, inv;          // lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
+    float one;                // 1 (its value is not for the compiler to know)
     uint32_t step_key;
     long long step_host;
     const float *grad_scale;

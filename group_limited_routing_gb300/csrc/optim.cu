@@ -37,7 +37,7 @@ constexpr int ADAM_THREADS = 128;
 constexpr int WARP_UNIT = ADAM_UNIT / (ADAM_THREADS / 32);      // a warp's elements
 
 struct Step {
-    float b1, one_b1, b2, one_b2, eps, size, inv, scale;
+    float b1, one_b1, b2, one_b2, eps, size, inv, scale, one;
     float decay;
     bool scaled;
     uint32_t step_key;
@@ -78,6 +78,9 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
     return r;
 }
+// a + b of a product a, with one = 1 that the compiler does not know: the assembler makes
+// one instruction of mul.rn.f32x2 and add.rn.f32x2, with one rounding
+__device__ __forceinline__ F2 add2_apart(F2 a, F2 b, F2 one) { return fma2(a, one, b); }
 __device__ __forceinline__ F2 add2_cut(F2 a, F2 b)
 {
     F2 r;
@@ -381,7 +384,7 @@ __device__ __forceinline__ void step_unit(const AdamTensor &t, const Step &c, lo
     }
     const uint32_t start = (uint32_t)il * 0x9E3779B9u + (t.key + c.step_key);
     const F2 one_b1 = f2(c.one_b1), one_b2 = f2(c.one_b2), inv = f2(c.inv), eps = f2(c.eps), size = f2(-c.size),
-             decay = f2(c.decay), tiny = f2(0x1p-16f);
+             decay = f2(c.decay), tiny = f2(0x1p-16f), one = f2(c.one);
 #pragma unroll
     for (int k = 0; k < PIECES; ++k) {
         const int i = 32 * V * k, left = rest - i;
@@ -419,8 +422,8 @@ __device__ __forceinline__ void step_unit(const AdamTensor &t, const Step &c, lo
             F2 gr = pair_of<V, GB>(g[k], h);
             if (c.scaled)
                 gr = mul2(gr, f2(c.scale));
-            mp[h] = add2(mul2(mp[h], b1), mul2(gr, one_b1));
-            vp[h] = add2(mul2(vp[h], b2), mul2(mul2(gr, gr), one_b2));
+            mp[h] = add2_apart(mul2(mp[h], b1), mul2(gr, one_b1), one);
+            vp[h] = add2_apart(mul2(vp[h], b2), mul2(mul2(gr, gr), one_b2), one);
             const F2 rt = sqrt2(vp[h]);
             // the update: a reciprocal to an ulp and three roundings, 2^-22 of it at most
             const float2 den = of(fma2(rt, inv, eps));
@@ -525,6 +528,7 @@ __global__ void __launch_bounds__(ADAM_THREADS, S8 ? 6 : 4) adamw_kernel(const _
     c.eps = k.eps;
     c.size = k.size;
     c.inv = k.inv;
+    c.one = k.one;
     c.step_key = k.step_key;
     c.scaled = k.grad_scale != nullptr;
     c.scale = c.scaled ? *k.grad_scale : 1.0f;
