@@ -100,27 +100,29 @@ __device__ __forceinline__ float rsqrt_approx(float x)
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ float min_nan(float a, float b)
+// Correctly rounded square roots of two values under 2^62, by Goldschmidt's iteration
+// with the correction of Markstein (1990): from y = 1 / sqrt(x) to 2^-22, g = x y and
+// h = y / 2 are refined together, then the residual x - g^2, exact in a fused
+// multiply-add, times h corrects g.  It all happens at 2^64 times the value, whose
+// residual does not underflow (2^-126 more for the rsqrt is nothing there, but keeps
+// zero's finite); a value past 2^64 gives NaN or is past 2^32.
+__device__ __forceinline__ F2 root2(F2 v)
 {
-    float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
+    const F2 x = mul2(v, f2(0x1p64f));
+    const float2 a = of(add2(x, f2(0x1p-126f)));
+    const F2 y = f2(rsqrt_approx(a.x), rsqrt_approx(a.y));
+    F2 g = mul2(x, y), h = mul2(y, f2(-0.5f));
+    const F2 r = fma2(g, h, f2(0.5f));
+    g = fma2(g, r, g);
+    h = fma2(h, r, h);
+    return mul2(fma2(fma2(g, g, mul2(x, f2(-1.0f))), h, g), f2(0x1p-32f));
 }
 
-// Square roots of two values: the hardware's h = 1 / sqrt(4 x) to about 2^-22, then
-// the residual of the root 2 x h, exact in a fused multiply-add, corrects it
-// (Markstein 1990).  That is the correctly rounded root but for about one value in a
-// million (and values under 2^-102, to 2 ulp).  Infinity counts as 2^125.
-__device__ __forceinline__ F2 sqrt2(F2 x)
+// ... of any value (zeros, of gradients that never came, are common).
+__device__ __forceinline__ float root_of(float v)
 {
-    const float2 v = of(x);
-    const float a = min_nan(v.x, 0x1p125f), b = min_nan(v.y, 0x1p125f);
-    const F2 c = f2(a, b), c2 = add2(c, c);
-    const float2 c4 = of(add2(c2, c2));
-    const F2 h = f2(rsqrt_approx(c4.x + 0x1p-126f), rsqrt_approx(c4.y + 0x1p-126f));   // (not of zero)
-    const F2 s = mul2(c2, h);
-    const float2 r = of(s);
-    return fma2(f2(fmaf(-r.x, r.x, a), fmaf(-r.y, r.y, b)), h, s);
+    const float r = __fsqrt_rn(v == 0.0f ? 1.0f : v);
+    return v == 0.0f ? v : r;
 }
 
 // Odd multipliers from the fractional parts of the golden ratio and of the square
@@ -260,21 +262,22 @@ __device__ __forceinline__ float scale_value(uint32_t b)
     return __uint_as_float(max(b << 23, 0x00400000u));
 }
 
-// the larger magnitude, or NaN if one is
-__device__ __forceinline__ float max_magnitude(float a, float b)
+// the largest magnitude, or NaN if one is
+template <int V>
+__device__ __forceinline__ float largest(const float (&x)[V])
 {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
-    return r;
+    float t = x[0];
+#pragma unroll
+    for (int i = 1; i < V; i += 2)
+        asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(t) : "f"(fabsf(t)), "f"(fabsf(x[i])), "f"(fabsf(x[(i + 1) % V])));
+    return t;
 }
 
 // What the scale of a block follows from, in 9 bits and in order of the magnitude:
 // block_scale's byte is the key - 9 (0 at least); 0 for zero, 256 for an infinity or a
 // NaN.  (A carry out of the mantissa past 0.875.)
-__device__ __forceinline__ uint32_t scale_key(const float (&x)[8])
+__device__ __forceinline__ uint32_t scale_key(float t)
 {
-    const float t = max_magnitude(max_magnitude(max_magnitude(x[0], x[1]), max_magnitude(x[2], x[3])),
-                                  max_magnitude(max_magnitude(x[4], x[5]), max_magnitude(x[6], x[7])));
     const uint32_t top = __float_as_uint(t);
     return top ? min(((top + 0x1fffffu) >> 23) + 1u, 256u) : 0u;
 }
@@ -342,8 +345,11 @@ __device__ __forceinline__ void quantize(const float (&x)[8], const uint32_t (&b
 // A warp's elements, V to a lane at a time: four, or with 8-bit states eight, so that 16
 // lanes hold a block of 128 and what belongs to a block (its scales, their keys) is
 // done once for eight elements.
-template <int KIND, bool WHOLE>
-__device__ __forceinline__ void step_unit(const AdamTensor &t, const Step &c, long long i0)
+// WHOLE: all of them exist, on vector boundaries.  FAST: by root2; the result has
+// a bit for each piece with a value that it is not for, of which nothing is written.
+//  Otherwise the pieces of `pieces`, any value.
+template <int KIND, bool WHOLE, bool FAST>
+__device__ __forceinline__ uint32_t step_unit(const AdamTensor &t, const Step &c, long long i0, uint32_t pieces)
 {
     constexpr bool S8 = KIND & K_S8, PB = KIND & K_PB, GB = KIND & K_GB, MASTER = KIND & K_MASTER;
     constexpr int V = S8 ? 8 : 4, PIECES = WARP_UNIT / (32 * V);
@@ -361,7 +367,7 @@ __device__ __forceinline__ void step_unit(const AdamTensor &t, const Step &c, lo
 #pragma unroll
     for (int k = 0; k < PIECES; ++k) {
         const int i = 32 * V * k, left = rest - i;
-        if (!WHOLE && i >= there)
+        if (!WHOLE && (i >= there || (!FAST && !(pieces >> k & 1))))
             continue;
         load<V, GB, WHOLE>(pg, i, left, g[k]);
         if (MASTER)
@@ -382,17 +388,19 @@ __device__ __forceinline__ void step_unit(const AdamTensor &t, const Step &c, lo
             load<V, false, WHOLE>(pv, i, left, v[k]);
         }
     }
+    uint32_t odd = 0;
     const uint32_t start = (uint32_t)il * 0x9E3779B9u + (t.key + c.step_key);
     const F2 one_b1 = f2(c.one_b1), one_b2 = f2(c.one_b2), inv = f2(c.inv), eps = f2(c.eps), size = f2(-c.size),
              decay = f2(c.decay), tiny = f2(0x1p-16f), one = f2(c.one);
 #pragma unroll
     for (int k = 0; k < PIECES; ++k) {
         const int i = 32 * V * k, left = rest - i;
-        if (!WHOLE && i >= there)
+        if (!WHOLE && (i >= there || (!FAST && !(pieces >> k & 1))))
             continue;
         float mk[V], vk[V], wk[V], root[V];
         uint32_t bits[V];
-        F2 b1 = f2(c.b1), b2 = f2(c.b2), mp[V / 2], vp[V / 2];
+        F2 b1 = f2(c.b1), b2 = f2(c.b2);
+        F2 mp[V / 2], vp[V / 2];
         if (S8) {
             // the scales are powers of two: times beta first, exactly; a root of 4
             // bits has an exact square
@@ -424,16 +432,27 @@ __device__ __forceinline__ void step_unit(const AdamTensor &t, const Step &c, lo
                 gr = mul2(gr, f2(c.scale));
             mp[h] = add2_apart(mul2(mp[h], b1), mul2(gr, one_b1), one);
             vp[h] = add2_apart(mul2(vp[h], b2), mul2(mul2(gr, gr), one_b2), one);
-            const F2 rt = sqrt2(vp[h]);
-            // the update: a reciprocal to an ulp and three roundings, 2^-22 of it at most
-            const float2 den = of(fma2(rt, inv, eps));
-            const F2 update = mul2(mp[h], f2(rcp_approx(den.x), rcp_approx(den.y)));
-            const float2 wn = of(fma2(update, size, mul2(pair_of<V, PB && !MASTER>(w[k], h), decay)));
-            const float2 mn = of(mp[h]), vn = of(vp[h]), rn = of(rt);
-            wk[2 * h] = wn.x, wk[2 * h + 1] = wn.y;
+            const float2 mn = of(mp[h]), vn = of(vp[h]);
+            const float2 rn = FAST ? of(root2(vp[h])) : make_float2(root_of(vn.x), root_of(vn.y));
             mk[2 * h] = mn.x, mk[2 * h + 1] = mn.y;
             vk[2 * h] = vn.x, vk[2 * h + 1] = vn.y;
             root[2 * h] = rn.x, root[2 * h + 1] = rn.y;
+        }
+        if (!WHOLE)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (j >= left)
+                    mk[j] = root[j] = 0.0f;          // (past the end: no part of the block's largest)
+        const float mtop = largest(mk), rtop = largest(root);
+        const bool mine = !FAST || __all_sync(0xffffffffu, rtop < 0x1p30f);
+        odd |= mine ? 0u : 1u << k;
+#pragma unroll
+        for (int h = 0; h < V / 2; ++h) {
+            // the update: a reciprocal to an ulp and three roundings, 2^-22 of it at most
+            const float2 den = of(fma2(f2(root[2 * h], root[2 * h + 1]), inv, eps));
+            const F2 update = mul2(mp[h], f2(rcp_approx(den.x), rcp_approx(den.y)));
+            const float2 wn = of(fma2(update, size, mul2(pair_of<V, PB && !MASTER>(w[k], h), decay)));
+            wk[2 * h] = wn.x, wk[2 * h + 1] = wn.y;
         }
 #pragma unroll
         for (int q = 0; q < V; ++q)
@@ -442,30 +461,29 @@ __device__ __forceinline__ void step_unit(const AdamTensor &t, const Step &c, lo
         if constexpr (S8) {
             uint2 q;
             uint32_t s;
-            if (!WHOLE)
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if (j >= left)
-                        mk[j] = root[j] = 0.0f;      // (past the end: no part of the block's largest)
             // both keys of the block over its 16 lanes
-            uint32_t keys = scale_key(mk) | (scale_key(root) << 16);
+            uint32_t keys = scale_key(mtop) | (scale_key(rtop) << 16);
 #pragma unroll
             for (int off = 8; off; off >>= 1)
                 keys = __vmaxu2(keys, __shfl_xor_sync(0xffffffffu, keys, off));
-            const bool writes = (lane & 15) == 0 && (WHOLE || left > 0);
+            const bool writes = mine && (lane & 15) == 0 && (WHOLE || left > 0);
             quantize<false>(mk, bits, keys & 0xffffu, tiny, q, s);
-            store_bytes<WHOLE>(pm, i, left, q);
+            if (mine)
+                store_bytes<WHOLE>(pm, i, left, q);
             if (writes)
                 ps[2 * k] = (uint8_t)s;
             quantize<true>(root, bits, keys >> 16, tiny, q, s);
-            store_bytes<WHOLE>(pv, i, left, q);
+            if (mine)
+                store_bytes<WHOLE>(pv, i, left, q);
             if (writes)
                 pr[2 * k] = (uint8_t)s;
         } else {
-            store<V, WHOLE>(pm, i, left, mk);
-            store<V, WHOLE>(pv, i, left, vk);
+            if (mine)
+                store<V, WHOLE>(pm, i, left, mk);
+            if (mine)
+                store<V, WHOLE>(pv, i, left, vk);
         }
-        if (MASTER)
+        if (MASTER && mine)
             store<V, WHOLE>(pw, i, left, wk);
         if (PB) {
             uint32_t h[V / 2];
@@ -494,20 +512,33 @@ __device__ __forceinline__ void step_unit(const AdamTensor &t, const Step &c, lo
                 for (int q = 0; q < V / 2; ++q)
                     h[q] = __byte_perm(x[2 * q], x[2 * q + 1], 0x7632);
             }
-            store_bf16<V, WHOLE>(pp, i, left, h);
-        } else {
+            if (mine)
+                store_bf16<V, WHOLE>(pp, i, left, h);
+        } else if (mine) {
             store<V, WHOLE>(pp, i, left, wk);
         }
     }
+    return odd;
+}
+
+// (a call, so that the 8-bit kernel's registers go to what all but such pieces need)
+template <int KIND>
+__device__ __noinline__ void step_rest(const AdamTensor &t, const Step &c, long long i0, uint32_t pieces)
+{
+    step_unit<KIND, false, false>(t, c, i0, pieces);
 }
 
 template <int KIND>
 __device__ __forceinline__ void step_any(const AdamTensor &t, const Step &c, long long i0)
 {
-    if ((t.kind & K_VEC) && i0 + WARP_UNIT <= t.n)
-        step_unit<KIND, true>(t, c, i0);
+    const uint32_t rest = (t.kind & K_VEC) && i0 + WARP_UNIT <= t.n ? step_unit<KIND, true, true>(t, c, i0, 0)
+                                                                    : step_unit<KIND, false, true>(t, c, i0, 0);
+    if (__builtin_expect(rest == 0, 1))
+        return;
+    if constexpr (KIND & K_S8)
+        step_rest<KIND>(t, c, i0, rest);
     else
-        step_unit<KIND, false>(t, c, i0);
+        step_unit<KIND, false, false>(t, c, i0, rest);
 }
 
 // A kernel for each kind of state.  Blocks of 128 threads.  With 8-bit states 2^26

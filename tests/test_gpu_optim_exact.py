@@ -58,3 +58,94 @@ def test_moments_are_rounded_operation_by_operation(lo, hi):
     got = stepped(p, g, m, v, 1e-3, b1, b2, 1e-8)
     want = formula(p, g, m, v, 1, 1e-3, b1, b2, 1e-8, 0.0)
     assert np.array_equal(got[1], want[1]) and np.array_equal(got[2], want[2])
+
+
+def every_exponent(seed):
+    """Values of every exponent, zero, the largest numbers, infinity and NaN."""
+    rng = np.random.default_rng(seed)
+    bits = (np.arange(255, dtype=np.uint32)[:, None] << 23) | rng.integers(0, 1 << 23, (255, 64), dtype=np.uint32)
+    ends = np.array([0, 1, 2, 0x7fffff, 0x800000, 0x7f7fffff, 0x7f800000, 0x7fc00000], np.uint32)
+    return np.concatenate([bits.ravel(), ends]).view(f)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-8])
+def test_roots_of_every_size(eps):
+    """No second moment is too large or too small for its root: an infinite one stops
+    the parameter, a subnormal one moves it by lr."""
+    v = every_exponent(1)
+    n = v.size
+    m = (np.where(np.isfinite(v) & (v > 0), np.sqrt(v), f(1)) * np.random.default_rng(2).uniform(0.5, 2, n)).astype(f)
+    zero = np.zeros(n, f)
+    got = stepped(zero, zero, m, v, 1.0, 0.5, 0.5, eps)[0]
+    with np.errstate(all="ignore"):
+        m, v = m * f(0.5), v * f(0.5)
+        root = np.sqrt(v).astype(np.float64)
+        want = -(m.astype(np.float64) / (root / math.sqrt(0.5) + eps)) / 0.5
+    ends = ~np.isfinite(v) | (want == 0)
+    assert np.array_equal(got[ends], want[ends].astype(f), equal_nan=True)
+    # a rounding each of the root, 1 / sqrt(1 - beta2), their product, eps and the sum,
+    # the quotient and twice the product with lr: eight halves of a step at most
+    with np.errstate(all="ignore"):
+        far = np.abs(got - want) / np.abs(want)
+    inf = np.isinf(want)
+    assert np.array_equal(got[inf], want[inf].astype(f))
+    assert far[~ends & ~inf].max() <= 8 * 2.0 ** -24
+
+
+def random_bits(n, key):
+    x = (np.arange(n, dtype=np.uint64) * np.uint64(0x9E3779B9) + np.uint64(key)) & np.uint64(0xffffffff)
+    for shift, times in ((16, 0x6A09E667), (15, 0xBB67AE85)):
+        x ^= x >> np.uint64(shift)
+        x = (x * np.uint64(times)) & np.uint64(0xffffffff)
+    return x ^ (x >> np.uint64(16))
+
+
+def key(seed, step, ordinal=0):
+    return (seed + step * 0x85A308D3 + ordinal * 0x13198A2F) & 0xffffffff
+
+
+def to_bytes(x, u, up):
+    """x [n] fp32 -> (e4m3 values, scale bytes) by the rounding rule (the sum with the
+    random fraction rounded to fp32, all else exact)."""
+    n = x.size
+    b = np.pad(x.astype(np.float64), (0, -n % 128)).reshape(-1, 128)
+    top = np.abs(b).max(1)
+    bad = ~np.isfinite(top)
+    m, e = np.frexp(np.where(bad, 1.0, top) / 448.0)
+    e = np.maximum(np.where(top > 0, np.where(m == 0.5, e - 1, e), 0), -127)
+    t = np.abs(np.where(bad[:, None], 0.0, b)) / np.exp2(e.astype(np.float64))[:, None]
+    step = np.exp2(np.maximum(np.frexp(t)[1] - 1, -6) - 3.0)
+    fraction = np.pad(u.astype(np.float64), (0, -n % 128)).reshape(-1, 128) / 65536
+    q = np.floor((t / step).astype(f) + fraction.astype(f)).astype(np.float64)
+    if up:
+        q = np.where((q == 0) & (t > 0), 1.0, q)
+    q = np.where(bad[:, None], np.nan, np.sign(b) * q * step)
+    return q.ravel()[:n], np.where(bad, 255, e + 127)
+
+
+def check_bytes(opt, i, name, x, u, up):
+    q, scale = to_bytes(x, u, up)
+    assert np.array_equal(opt.state[name + "_scale"][i].view(torch.uint8).cpu().numpy(), scale)
+    assert np.array_equal(host(opt.state[name][i]), q.astype(f), equal_nan=True)
+
+
+def spread(opt, i, name):
+    """The values that 8-bit states stand for (exact in fp32 but for the smallest)."""
+    q, s = opt.state[name][i].double(), opt.state[name + "_scale"][i].double()
+    return (q * s.repeat_interleave(128)[:q.numel()]).cpu().numpy().astype(f)
+
+
+@pytest.mark.parametrize("lo,hi", [(-20, 0), (60, 66), (80, 100)])
+def test_large_roots_in_8_bits(lo, hi):
+    """The root of a square past fp32's range is infinite, and so its block's scale NaN."""
+    n, b1, b2 = 4000, 0.9, 0.999
+    g = gradient_sizes(n, 3, lo, hi)
+    zero = np.zeros(n, f)
+    p = on(zero)
+    opt = optim.AdamW([p], lr=1e-3, betas=(b1, b2), weight_decay=0.0, state_bits=8, seed=5)
+    opt.step([on(g)])
+    want, m, v, root = formula(zero, g, zero, zero, 1, 1e-3, b1, b2, 1e-8, 0.0)
+    bits = random_bits(n, key(5, 1))
+    check_bytes(opt, 0, "m", m, bits & np.uint64(0xffff), False)
+    check_bytes(opt, 0, "v", root, bits >> np.uint64(16), True)
+    assert np.abs(host(p) - want).max() <= 2.0 ** -20 * np.abs(want).max()
