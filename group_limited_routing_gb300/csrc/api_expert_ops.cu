@@ -170,7 +170,8 @@ cudaError_t adamw_chunk(const moe_adamw_tensor *t, int count, const AdamScalars 
         a.v_scale = t[i].v_scale;
         a.n = t[i].n;
         a.weight_decay = t[i].weight_decay;
-        a.decay = (float)(1.0 - c.lr * t[i].weight_decay);
+        const volatile double shrink = c.lr * t[i].weight_decay;     // (two roundings, on every host)
+        a.decay = (float)(1.0 - shrink);
         a.key = seed + t[i].ordinal * 0x13198A2Fu;
         const bool vec = aligned(a.p, pb && !bytes ? 8 : 16) && aligned(a.g, gb && !bytes ? 8 : 16) &&
                          aligned(a.master, 16) && aligned(a.m, bytes ? 8 : 16) && aligned(a.v, bytes ? 8 : 16);

@@ -4,9 +4,10 @@
 //   m <- beta1 m + (1 - beta1) g,  v <- beta2 v + (1 - beta2) g^2
 //   p <- p (1 - lr decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
 //
-// in fp32.  m and v are rounded operation by operation in this order (no fused
-// multiply-adds) and the root is correctly rounded, so that they do not depend on
-// how a compiler groups them: 8-bit states then round the same way everywhere.
+// in fp32, each operation correctly rounded by itself in this order (no fused
+// multiply-adds), so that the results do not depend on how a compiler groups them: an
+// ulp would put a few of the values that are then rounded stochastically on the other
+// side of a border.  (A quotient under 2^-126 is not rounded to a subnormal number.)
 //
 // 8-bit states hold m and sqrt(v) as e4m3 with a power-of-two scale for each 128
 // elements.  The root halves the range of v's exponents: within a block e4m3
@@ -39,7 +40,7 @@ constexpr int WARP_UNIT = ADAM_UNIT / (ADAM_THREADS / 32);      // a warp's elem
 struct Step {
     float b1, one_b1, b2, one_b2, eps, size, inv, scale, one;
     float decay;
-    bool scaled;
+    bool scaled, plain;
     uint32_t step_key;
 };
 
@@ -118,11 +119,29 @@ __device__ __forceinline__ F2 root2(F2 v)
     return mul2(fma2(fma2(g, g, mul2(x, f2(-1.0f))), h, g), f2(0x1p-32f));
 }
 
-// ... of any value (zeros, of gradients that never came, are common).
+// Correctly rounded m / -a of two values each (Markstein 1990): a reciprocal refined
+// until it is the rounded one, then the quotient corrected by its exact residual.
+// 2^-85 <= |m| < 2^74 or m = 0, 2^-50 <= -a < 2^41.
+__device__ __forceinline__ F2 quotient2(F2 m, F2 a)
+{
+    const float2 n = of(a);
+    F2 z = f2(rcp_approx(-n.x), rcp_approx(-n.y));
+    z = fma2(z, fma2(a, z, f2(1.0f)), z);
+    const F2 q = mul2(m, z);
+    return fma2(fma2(a, q, m), z, q);
+}
+
+// Both for any value (the zeros of a gradient that never came are common).
 __device__ __forceinline__ float root_of(float v)
 {
     const float r = __fsqrt_rn(v == 0.0f ? 1.0f : v);
     return v == 0.0f ? v : r;
+}
+__device__ __forceinline__ float quotient(float m, float den)
+{
+    const bool zero = m == 0.0f && den > 0.0f;
+    const float q = __fdiv_rn(zero ? 1.0f : m, zero ? 1.0f : den);
+    return zero ? m : q;
 }
 
 // Odd multipliers from the fractional parts of the golden ratio and of the square
@@ -345,9 +364,9 @@ __device__ __forceinline__ void quantize(const float (&x)[8], const uint32_t (&b
 // A warp's elements, V to a lane at a time: four, or with 8-bit states eight, so that 16
 // lanes hold a block of 128 and what belongs to a block (its scales, their keys) is
 // done once for eight elements.
-// WHOLE: all of them exist, on vector boundaries.  FAST: by root2; the result has
-// a bit for each piece with a value that it is not for, of which nothing is written.
-//  Otherwise the pieces of `pieces`, any value.
+// WHOLE: all of them exist, on vector boundaries.  FAST: by root2 and quotient2; the
+// result has a bit for each piece with a value that these are not for, of which nothing
+// is written.  Otherwise the pieces of `pieces`, any value.
 template <int KIND, bool WHOLE, bool FAST>
 __device__ __forceinline__ uint32_t step_unit(const AdamTensor &t, const Step &c, long long i0, uint32_t pieces)
 {
@@ -390,8 +409,8 @@ __device__ __forceinline__ uint32_t step_unit(const AdamTensor &t, const Step &c
     }
     uint32_t odd = 0;
     const uint32_t start = (uint32_t)il * 0x9E3779B9u + (t.key + c.step_key);
-    const F2 one_b1 = f2(c.one_b1), one_b2 = f2(c.one_b2), inv = f2(c.inv), eps = f2(c.eps), size = f2(-c.size),
-             decay = f2(c.decay), tiny = f2(0x1p-16f), one = f2(c.one);
+    const F2 one_b1 = f2(c.one_b1), one_b2 = f2(c.one_b2), ninv = f2(-c.inv), neps = f2(-c.eps),
+             size = f2(c.size * -0x1p-64f), decay = f2(c.decay), tiny = f2(0x1p-16f), one = f2(c.one);
 #pragma unroll
     for (int k = 0; k < PIECES; ++k) {
         const int i = 32 * V * k, left = rest - i;
@@ -444,15 +463,24 @@ __device__ __forceinline__ uint32_t step_unit(const AdamTensor &t, const Step &c
                 if (j >= left)
                     mk[j] = root[j] = 0.0f;          // (past the end: no part of the block's largest)
         const float mtop = largest(mk), rtop = largest(root);
-        const bool mine = !FAST || __all_sync(0xffffffffu, rtop < 0x1p30f);
+        const bool mine = !FAST || __all_sync(0xffffffffu, c.plain && mtop < 0x1p10f && rtop < 0x1p30f);
         odd |= mine ? 0u : 1u << k;
 #pragma unroll
         for (int h = 0; h < V / 2; ++h) {
-            // the update: a reciprocal to an ulp and three roundings, 2^-22 of it at most
-            const float2 den = of(fma2(f2(root[2 * h], root[2 * h + 1]), inv, eps));
-            const F2 update = mul2(mp[h], f2(rcp_approx(den.x), rcp_approx(den.y)));
-            const float2 wn = of(fma2(update, size, mul2(pair_of<V, PB && !MASTER>(w[k], h), decay)));
-            wk[2 * h] = wn.x, wk[2 * h + 1] = wn.y;
+            const F2 wo = pair_of<V, PB && !MASTER>(w[k], h), rt = f2(root[2 * h], root[2 * h + 1]);
+            if (FAST) {
+                const F2 u = quotient2(mul2(mp[h], f2(0x1p64f)), add2_apart(mul2(rt, ninv), neps, one));
+                const float2 wn = of(add2_apart(mul2(u, size), mul2(wo, decay), one));
+                wk[2 * h] = wn.x, wk[2 * h + 1] = wn.y;
+            } else {
+                const float2 wf = of(wo);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int q = 2 * h + j;
+                    const float u = quotient(mk[q], __fadd_rn(__fmul_rn(root[q], c.inv), c.eps));
+                    wk[q] = __fsub_rn(__fmul_rn(j ? wf.y : wf.x, c.decay), __fmul_rn(u, c.size));
+                }
+            }
         }
 #pragma unroll
         for (int q = 0; q < V; ++q)
@@ -590,6 +618,8 @@ __global__ void __launch_bounds__(ADAM_THREADS, S8 ? 6 : 4) adamw_kernel(const _
         if (k.step)
             c.step_key = (uint32_t)*k.step * 0x85A308D3u;
     }
+    // (what root2, quotient2 and the factor 2^-64 of size are for)
+    c.plain = c.inv < 0x1p10f && c.eps >= 0x1p-50f && c.eps < 0x1p30f && (c.size == 0.0f || fabsf(c.size) >= 0x1p-62f);
     if (!(fabsf(c.scale) <= 3.402823466e38f))
         return;                                  // (a step whose gradients' norm is not finite is left out)
     const long long i0 = (long long)((int)blockIdx.x - tab.unit0[lo]) * ADAM_UNIT + (threadIdx.x >> 5) * WARP_UNIT;

@@ -576,7 +576,9 @@ int moe_scaled_weight_gradient(int32_t M, int32_t N, int64_t P, int32_t E, int32
  * One step over `count` tensors (a HOST array), each of n elements:
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
  *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
- * in fp32, m and v rounded operation by operation.  flags:
+ * in fp32, each operation correctly rounded by itself (1 - lr weight_decay, lr / (1 -
+ * beta1^step) and 1 / sqrt(1 - beta2^step) in 64 bits first; a quotient under 2^-126 is
+ * not rounded to a subnormal number).  flags:
  *   MOE_ADAMW_STATES_IN_BYTES  m [n] holds m and v [n] holds sqrt(v) in e4m3, with
  *       m_scale, v_scale [ceil(n / 128)]: bytes as in moe_scaled_quantize, a scale
  *       for each 128 elements; rounded stochastically (a root that is not zero

@@ -149,3 +149,74 @@ def test_large_roots_in_8_bits(lo, hi):
     check_bytes(opt, 0, "m", m, bits & np.uint64(0xffff), False)
     check_bytes(opt, 0, "v", root, bits >> np.uint64(16), True)
     assert np.abs(host(p) - want).max() <= 2.0 ** -20 * np.abs(want).max()
+
+
+@pytest.mark.parametrize("lr,b1,b2,eps,decay", [(1e-3, 0.9, 0.999, 1e-8, 0.1), (0.3, 0.8, 0.95, 1e-15, 0.0),
+                                                (1e-3, 0.0, 0.5, 0.0, 0.1), (1e-25, 0.9, 0.99, 1e-30, 0.1)])
+@pytest.mark.parametrize("lo,hi", [(-16, 0), (-45, 70)])
+def test_a_step_is_the_formula_to_the_bit(lo, hi, lr, b1, b2, eps, decay):
+    n = 200003
+    p, g = gradient_sizes(n, 4, -6, 0), gradient_sizes(n, 5, lo, hi)
+    m, v = gradient_sizes(n, 6, lo, hi), np.square(gradient_sizes(n, 7, max(lo, -40), hi / 2))
+    p[:300], g[128:512], m[256:900], v[384:700] = 0, 0, 0, 0
+    got = stepped(p, g, m, v, lr, b1, b2, eps, decay, step=6)
+    want = formula(p, g, m, v, 7, lr, b1, b2, eps, decay)
+    for a, b in zip(got, want):
+        assert np.array_equal(a, b, equal_nan=True)
+
+
+def test_every_mantissa():
+    """All roots of a binade pair, and all quotients by them with some numerators:
+    those of 1 are the reciprocals, on which the other quotients' rounding rests."""
+    v = np.arange(1 << 24, dtype=np.uint32) + np.uint32(0x40000000)      # 2 to 8, halved by the step
+    v = v.view(f)
+    zero = np.zeros(v.size, f)
+    rng = np.random.default_rng(8)
+    for m in (np.full(v.size, 2, f), (rng.standard_normal(v.size) * np.exp2(rng.uniform(-30, 8, v.size))).astype(f)):
+        got = stepped(zero, zero, m, v, 1.0, 0.5, 0.5, 1e-15, step=10 ** 6)     # 1 - beta^t is 1
+        want = formula(zero, zero, m, v, 10 ** 6 + 1, 1.0, 0.5, 0.5, 1e-15, 0.0)
+        assert np.array_equal(got[0], want[0])
+    # many numerators over the divisors next to a power of two
+    roots = np.concatenate([np.nextafter(f(2), f(0), dtype=f) - np.arange(8, dtype=f) * f(2.0 ** -23),
+                            f(1) + np.arange(8, dtype=f) * f(2.0 ** -23)])
+    v = np.square(roots.astype(np.float64)).astype(f)
+    keep = np.sqrt(v) == roots
+    assert keep.sum() >= 8
+    v = (v[keep] * f(2)).repeat(1 << 16)
+    m = rng.uniform(2, 4, v.size).astype(f)
+    zero = np.zeros(v.size, f)
+    got = stepped(zero, zero, m, v, 1.0, 0.5, 0.5, 1e-15, step=10 ** 6)
+    want = formula(zero, zero, m, v, 10 ** 6 + 1, 1.0, 0.5, 0.5, 1e-15, 0.0)
+    assert np.array_equal(got[0], want[0])
+
+
+@pytest.mark.parametrize("grad", [BF, F32])
+@pytest.mark.parametrize("param,master", [(BF, False), (BF, True), (F32, False)])
+@pytest.mark.parametrize("lo,hi", [(-16, 0), (-60, 66)])
+def test_8_bit_steps_are_the_formula_to_the_bit(lo, hi, param, master, grad):
+    """Values in 8 bits and stochastically rounded parameters included: an ulp in fp32
+    would put some of them on the other side of a rounding's border."""
+    sizes = [1, 127, 128, 129, 513, 4097, 300001]
+    params = [on(gradient_sizes(n, 10 + n, -6, 0)).to(param) for n in sizes]
+    lr, b1, b2, eps, decay, seed = 1e-2, 0.9, 0.99, 1e-8, 0.1, 987654321
+    opt = optim.AdamW(params, lr=lr, betas=(b1, b2), eps=eps, weight_decay=decay, state_bits=8, master=master, seed=seed)
+    for t in (1, 2, 3):
+        grads = [on(gradient_sizes(n, 20 + t, lo, hi)).to(grad) for n in sizes]
+        for g in grads:
+            g[100:400] = 0
+        old = [(host(opt.state["master"][i] if master else p), spread(opt, i, "m"), spread(opt, i, "v"))
+               for i, p in enumerate(params)]
+        opt.step(grads)
+        for i, (w, m, root) in enumerate(old):
+            n = sizes[i]
+            want, m, v, root = formula(w, host(grads[i]), m, np.square(root), t, lr, b1, b2, eps, decay)
+            bits = random_bits(n, key(seed, t, i))
+            check_bytes(opt, i, "m", m, bits & np.uint64(0xffff), False)
+            check_bytes(opt, i, "v", root, bits >> np.uint64(16), True)
+            if param == F32 or master:
+                assert np.array_equal(host(opt.state["master"][i] if master else params[i]), want, equal_nan=True)
+                assert not master or np.array_equal(host(params[i]), host(opt.state["master"][i].to(BF)), equal_nan=True)
+                continue
+            u = (((bits * np.uint64(0x9E3779B9)) & np.uint64(0xffffffff)) >> np.uint64(16)).astype(np.int32)
+            rounded = ((want.view(np.int32) + u) & np.int32(-65536)).view(f)
+            assert np.array_equal(host(params[i]), np.where(np.isnan(want), want, rounded), equal_nan=True)
