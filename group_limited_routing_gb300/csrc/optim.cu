@@ -418,23 +418,21 @@ __device__ __forceinline__ uint32_t step_unit(const AdamTensor &t, const Step &c
             continue;
         float mk[V], vk[V], wk[V], root[V];
         uint32_t bits[V];
-        F2 b1 = f2(c.b1), b2 = f2(c.b2);
+        const F2 b1 = f2(c.b1), b2 = f2(c.b2);
         F2 mp[V / 2], vp[V / 2];
         if (S8) {
-            // the scales are powers of two: times beta first, exactly; a root of 4
-            // bits has an exact square
+            // the states' values, exactly (a root of 4 bits has an exact square, if not
+            // under 2^-149); times beta only then: a small scale may leave no bits for it
 #pragma unroll
             for (int h = 0; h < V / 4; ++h) {
                 unpack_e4m3(m[k][h], mk + 4 * h);
                 unpack_e4m3(v[k][h], vk + 4 * h);
             }
-            const F2 r = f2(scale_value(sv[k]));
-            b1 = mul2(b1, f2(scale_value(sm[k])));
-            b2 = mul2(mul2(b2, r), r);
+            const F2 r = f2(scale_value(sv[k])), q = f2(scale_value(sm[k]));
 #pragma unroll
             for (int h = 0; h < V / 2; ++h) {
-                mp[h] = f2(mk[2 * h], mk[2 * h + 1]);
-                vp[h] = f2(vk[2 * h], vk[2 * h + 1]);
+                mp[h] = mul2(f2(mk[2 * h], mk[2 * h + 1]), q);
+                vp[h] = mul2(f2(vk[2 * h], vk[2 * h + 1]), r);
                 vp[h] = mul2(vp[h], vp[h]);
             }
         } else {

@@ -220,3 +220,22 @@ def test_8_bit_steps_are_the_formula_to_the_bit(lo, hi, param, master, grad):
             u = (((bits * np.uint64(0x9E3779B9)) & np.uint64(0xffffffff)) >> np.uint64(16)).astype(np.int32)
             rounded = ((want.view(np.int32) + u) & np.int32(-65536)).view(f)
             assert np.array_equal(host(params[i]), np.where(np.isnan(want), want, rounded), equal_nan=True)
+
+
+@pytest.mark.parametrize("exponent", [-150, -136, -128, -120, -90])
+def test_the_smallest_states_in_8_bits(exponent):
+    """Scales down to the format's smallest, 2^-127, where fp32 is subnormal."""
+    n, b1, b2, seed = 1000, 0.9, 0.99, 3
+    zero = np.zeros(n, f)
+    p = on(zero)
+    opt = optim.AdamW([p], lr=1e-3, betas=(b1, b2), eps=1e-8, weight_decay=0.0, state_bits=8, seed=seed)
+    rng = np.random.default_rng(9)
+    for name in ("m", "v"):
+        opt.state[name + "_scale"][0].view(torch.uint8).copy_(on(np.full(-(-n // 128), max(0, 127 + exponent // (1 + (name == "v"))), np.uint8)))
+        opt.state[name][0].view(torch.uint8).copy_(on(rng.integers(1, 127, n, dtype=np.uint8)))
+    m, root = spread(opt, 0, "m"), spread(opt, 0, "v")
+    opt.step([on(zero)])
+    want, m, v, root = formula(zero, zero, m, np.square(root), 1, 1e-3, b1, b2, 1e-8, 0.0)
+    bits = random_bits(n, key(seed, 1))
+    check_bytes(opt, 0, "m", m, bits & np.uint64(0xffff), False)
+    check_bytes(opt, 0, "v", root, bits >> np.uint64(16), True)
