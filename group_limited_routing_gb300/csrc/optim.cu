@@ -293,12 +293,12 @@ __device__ __forceinline__ float largest(const float (&x)[V])
 }
 
 // What the scale of a block follows from, in 9 bits and in order of the magnitude:
-// block_scale's byte is the key - 9 (0 at least); 0 for zero, 256 for an infinity or a
+// block_scale's byte is the key - 9 (0 at least); 0 for zero, 511 for an infinity or a
 // NaN.  (A carry out of the mantissa past 0.875.)
 __device__ __forceinline__ uint32_t scale_key(float t)
 {
     const uint32_t top = __float_as_uint(t);
-    return top ? min(((top + 0x1fffffu) >> 23) + 1u, 256u) : 0u;
+    return top >= 0x7f800000u ? 511u : top ? ((top + 0x1fffffu) >> 23) + 1u : 0u;
 }
 
 // Two t (|t| <= 448) to the e4m3 grid, away from zero where the fraction of a step
@@ -339,7 +339,7 @@ __device__ __forceinline__ void quantize(const float (&x)[8], const uint32_t (&b
                                          uint32_t &scale)
 {
     scale = (uint32_t)max((int)key - 9, 0);
-    if (key - 1u >= 255u) {                      // zeros, an infinity or a NaN
+    if (key - 1u >= 256u) {                      // zeros, an infinity or a NaN
         scale = key ? 255u : 127u;
         q = key ? make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu) : make_uint2(0u, 0u);
         return;

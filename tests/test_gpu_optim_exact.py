@@ -239,3 +239,16 @@ def test_the_smallest_states_in_8_bits(exponent):
     bits = random_bits(n, key(seed, 1))
     check_bytes(opt, 0, "m", m, bits & np.uint64(0xffff), False)
     check_bytes(opt, 0, "v", root, bits >> np.uint64(16), True)
+
+
+def test_the_largest_first_moments_in_8_bits():
+    """A block's largest magnitude between 1.75 2^127 and fp32's largest number is no
+    infinity: its scale is 2^120."""
+    n, seed = 128 * 4, 3
+    g = np.full(n, 2.0 ** 100, f)
+    g[5], g[130], g[300], g[400] = MAX, -f(1.75 * 2.0 ** 127), np.nextafter(f(1.75 * 2.0 ** 127), f(np.inf)), np.inf
+    p = torch.zeros(n, device=DEV)
+    opt = optim.AdamW([p], lr=0.0, betas=(0.0, 0.9), weight_decay=0.0, state_bits=8, seed=seed)
+    opt.step([on(g)])
+    check_bytes(opt, 0, "m", g, random_bits(n, key(seed, 1)) & np.uint64(0xffff), False)
+    assert opt.state["m_scale"][0].view(torch.uint8).tolist() == [247, 246, 247, 255]
