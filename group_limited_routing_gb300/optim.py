@@ -157,15 +157,16 @@ class AdamW:
         self.last_launches = 0
 
     def _fill_table(self) -> None:
-        """The library's table of the parameters and their states."""
+        """The library's table of the parameters and their states (all of it, or with an
+        error what it was)."""
         n, dev, bits = len(self.params), self.device, self.state_bits
         _check_tensors(self.params, "params", dev)
-        self._table, self._cols = _table(n)
+        table, cols = _table(n)
         for i, p in enumerate(self.params):
             size = self._sizes[i]
             if p.shape != self._shapes[i]:
                 raise ValueError("params[%d] must have shape %s, got %s" % (i, tuple(self._shapes[i]), tuple(p.shape)))
-            t = self._table[i]
+            t = table[i]
             t.p, t.n, t.weight_decay, t.ordinal = p.data_ptr(), size, self._decay[i], i
             kind = torch.float8_e4m3fn if bits == 8 else _F32
             for name in self._names:
@@ -178,7 +179,7 @@ class AdamW:
                     t.master = _need(s, what, _F32, (size,), dev)
             t.flags = (_lib.MOE_ADAMW_STATES_IN_BYTES if bits == 8 else 0) | \
                       (_lib.MOE_ADAMW_PARAM_BF16 if p.dtype == _BF16 else 0)
-        self._flags = self._cols["flags"][:n].copy()
+        self._table, self._cols, self._flags = table, cols, cols["flags"][:n].copy()
         self._addresses = list(map(_address, self.params))
 
     def _new_state(self) -> dict:
