@@ -53,6 +53,13 @@ _type = operator.attrgetter("dtype")
 _shape = operator.attrgetter("shape")
 
 
+def _addresses_of(tensors) -> list:
+    try:
+        return list(map(_address, tensors))
+    except TypeError:                            # (a master that is None, beside an fp32 parameter)
+        return [t.data_ptr() if isinstance(t, torch.Tensor) else None for t in tensors]
+
+
 def _fill_grads(grads, table, device):
     """Checks the gradients, puts their addresses into a table and gives the flags of
     their types.  (Hundreds of small tensors: an attribute at a time over all.)"""
@@ -115,8 +122,9 @@ class AdamW:
     copies of bf16 parameters; without, they are rounded stochastically.  seed: of
     the random bits.  state: dict of lists (m, v, with 8 bits m_scale and v_scale,
     with master master: None for fp32 parameters) to continue from after `step`
-    steps, used in place (their memory is that of the construction); without, the
-    state of no step is made.
+    steps, used in place; without, the state of no step is made.  A step works on the
+    tensors that `params` and `state` hold then: others may take their places (the
+    replaced ones are let go by the next step).
 
     capturable=True keeps the step's number and lr in tensors on the device
     (step_count [1] int64, lr_now [1] fp32), which each step() advances and reads
@@ -144,9 +152,6 @@ class AdamW:
         self._shapes = [p.shape for p in self.params]
         self.state = self._new_state() if state is None else state
         names = ["m", "v"] + (["m_scale", "v_scale"] if state_bits == 8 else []) + (["master"] if master else [])
-        for name in names:
-            if len(self.state[name]) != n:
-                raise ValueError("state[%r] must have %d tensors, got %d" % (name, n, len(self.state[name])))
         self._names, self._decay = names, [float(d) for d in decay]
         self._fill_table()
         self._cfg = _lib.AdamwCfg(lr, self.betas[0], self.betas[1], eps, max(step, 1), seed & 0xffffffff, 0)
@@ -159,7 +164,10 @@ class AdamW:
     def _fill_table(self) -> None:
         """The library's table of the parameters and their states (all of it, or with an
         error what it was)."""
-        n, dev, bits = len(self.params), self.device, self.state_bits
+        n, dev, bits = len(self._sizes), self.device, self.state_bits
+        for name, held in [("params", self.params)] + [("state[%r]" % (s,), self.state[s]) for s in self._names]:
+            if len(held) != n:
+                raise ValueError("%s must have %d tensors, got %d" % (name, n, len(held)))
         _check_tensors(self.params, "params", dev)
         table, cols = _table(n)
         for i, p in enumerate(self.params):
@@ -180,7 +188,17 @@ class AdamW:
             t.flags = (_lib.MOE_ADAMW_STATES_IN_BYTES if bits == 8 else 0) | \
                       (_lib.MOE_ADAMW_PARAM_BF16 if p.dtype == _BF16 else 0)
         self._table, self._cols, self._flags = table, cols, cols["flags"][:n].copy()
-        self._addresses = list(map(_address, self.params))
+        # (kept, so that nothing else is given a replaced tensor's memory, and with it an
+        # address that step() knows, before step() has looked)
+        self._held = self._tensors()
+        self._addresses = _addresses_of(self._held)
+
+    def _tensors(self) -> list:
+        """The parameters' and states' tensors as they are now."""
+        held = [*self.params]
+        for name in self._names:
+            held += self.state[name]
+        return held
 
     def _new_state(self) -> dict:
         dev, sizes = self.device, self._sizes
@@ -202,10 +220,10 @@ class AdamW:
         grad_scale [1] fp32 on the device: what the gradients are multiplied by (not
         finite: nothing is written, though the step counts)."""
         grads = list(grads)
-        if len(grads) != len(self.params):
-            raise ValueError("%d gradients expected, got %d" % (len(self.params), len(grads)))
-        if list(map(_address, self.params)) != self._addresses:      # (a parameter was given other memory)
+        if _addresses_of(self._tensors()) != self._addresses:        # (one of them has other memory)
             self._fill_table()
+        if len(grads) != len(self._sizes):
+            raise ValueError("%d gradients expected, got %d" % (len(self._sizes), len(grads)))
         bits = _fill_grads(grads, self._cols, self.device)
         if list(map(_shape, grads)) != self._shapes:
             i = next(i for i, (g, s) in enumerate(zip(grads, self._shapes)) if g.shape != s)
