@@ -142,11 +142,22 @@ class AdamW:
             raise TypeError("params[0] must be a tensor")
         self.device = dev = self.params[0].device
         _check_tensors(self.params, "params", dev)
+        betas = tuple(betas)
+        if not math.isfinite(lr):
+            raise ValueError("lr must be finite, got %r" % (lr,))
+        if len(betas) != 2 or not all(0.0 <= b < 1.0 for b in betas):
+            raise ValueError("betas must be two numbers from 0 and below 1, got %r" % (betas,))
+        if not 0.0 <= eps < math.inf:
+            raise ValueError("eps must be finite and at least 0, got %r" % (eps,))
+        if step < 0:
+            raise ValueError("step must be at least 0, got %r" % (step,))
         n = len(self.params)
         decay = list(weight_decay) if hasattr(weight_decay, "__len__") else [weight_decay] * n
         if len(decay) != n:
             raise ValueError("weight_decay must be a number or %d of them, got %d" % (n, len(decay)))
-        self.lr, self.betas, self.eps, self.step_number, self.seed = lr, tuple(betas), eps, step, seed
+        if not all(0.0 <= d < math.inf for d in decay):
+            raise ValueError("weight_decay must be finite and at least 0, got %r" % (weight_decay,))
+        self.lr, self.betas, self.eps, self.step_number, self.seed = lr, betas, eps, step, seed
         self.state_bits, self.master = state_bits, master
         self._sizes = [p.numel() for p in self.params]
         self._shapes = [p.shape for p in self.params]
@@ -230,19 +241,26 @@ class AdamW:
             raise ValueError("grads[%d] must have shape %s, got %s" % (i, tuple(self._shapes[i]), tuple(grads[i].shape)))
         self._cols["flags"] = self._flags | bits
         ps = _opt(grad_scale, "grad_scale", _F32, (1,), self.device)
-        if lr is not None:
-            if not math.isfinite(lr):
-                raise ValueError("lr must be finite, got %r" % (lr,))
-            self.lr = lr
-            if self.lr_now is not None:
-                self.lr_now.fill_(lr)
-        self.step_number += 1
+        new_lr = self.lr if lr is None else lr
+        if not math.isfinite(new_lr):
+            raise ValueError("lr must be finite, got %r" % (new_lr,))
         cfg = self._cfg
-        cfg.lr, cfg.step = self.lr, self.step_number
+        cfg.lr, cfg.step = new_lr, self.step_number + 1
         pc = pl = None
         if self.step_count is not None:
+            if lr is not None:
+                self.lr_now.fill_(lr)
             self.step_count.add_(1)
             pc, pl = self.step_count.data_ptr(), self.lr_now.data_ptr()
-        _lib.check(_on(self.device, _lib.load().moe_adamw, len(grads), ctypes.addressof(self._table), ctypes.byref(cfg), ps,
-                       pc, pl), "moe_adamw")
+        try:
+            _lib.check(_on(self.device, _lib.load().moe_adamw, len(grads), ctypes.addressof(self._table), ctypes.byref(cfg),
+                           ps, pc, pl), "moe_adamw")
+        except Exception:                        # (what the kernel would have read counts no step either)
+            if self.step_count is not None:
+                self.step_count.sub_(1)
+                if lr is not None:
+                    self.lr_now.fill_(self.lr)
+            raise
+        self.lr = new_lr
+        self.step_number += 1
         self.last_launches = _lib.load().moe_last_launch_count()

@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from group_limited_routing_gb300 import optim
+from group_limited_routing_gb300 import _lib, optim
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -90,3 +90,25 @@ def test_states_that_do_not_fit_are_refused():
     assert opt.step_number == 0 and all(torch.equal(x, y) for x, y in zip(before, p))
     opt.step(grads)
     assert opt.step_number == 1 and not any(torch.equal(x, y) for x, y in zip(before, p))
+
+
+@pytest.mark.parametrize("capturable", [False, True])
+def test_a_step_that_the_library_refuses_does_not_count(capturable, monkeypatch):
+    a, b, grads = tensors(1), tensors(1), tensors(2)
+    oa, ob = [optim.AdamW(p, lr=0.1, capturable=capturable) for p in (a, b)]
+    with monkeypatch.context() as m:
+        m.setattr(_lib.load(), "moe_adamw", lambda *_: _lib.MOE_ERR_INVALID_ARG)
+        for kw in ({}, dict(lr=0.5)):
+            with pytest.raises(_lib.MoeError):
+                ob.step(grads, **kw)
+    ob.lr = math.nan
+    with pytest.raises(ValueError, match="lr"):
+        ob.step(grads)
+    ob.lr = 0.1
+    assert ob.step_number == 0
+    if capturable:
+        assert ob.step_count.item() == 0 and ob.lr_now.item() == oa.lr_now.item()
+    for opt in (oa, ob):
+        opt.step(grads)
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
