@@ -53,6 +53,16 @@ _type = operator.attrgetter("dtype")
 _shape = operator.attrgetter("shape")
 
 
+def _refuse_overlaps(named) -> None:
+    """Lists of (name, contiguous tensors or Nones) of which no two may share memory: the
+    kernel's blocks read and write all of them at once."""
+    spans = sorted((t.data_ptr(), t.numel() * t.element_size(), "%s[%d]" % (name, i)) for name, held in named
+                   for i, t in enumerate(held) if t is not None and t.numel())
+    for (a, size, first), (b, _, second) in zip(spans, spans[1:]):
+        if a + size > b:
+            raise ValueError("%s and %s overlap" % (first, second))
+
+
 def _addresses_of(tensors) -> list:
     try:
         return list(map(_address, tensors))
@@ -115,7 +125,7 @@ def grad_norm(grads, max_norm: float = 1.0, *, ws: Optional[SizedWorkspace] = No
 
 class AdamW:
     """AdamW over `params` (contiguous bf16 or fp32 tensors, which the steps change in
-    place).
+    place; no two of them, or of the states, may share memory).
 
     weight_decay: one for all, or one for each.  state_bits: 32 (m and v in fp32) or
     8 (m and sqrt(v) in e4m3 with scales for each 128 elements).  master: keep fp32
@@ -198,6 +208,7 @@ class AdamW:
                     t.master = _need(s, what, _F32, (size,), dev)
             t.flags = (_lib.MOE_ADAMW_STATES_IN_BYTES if bits == 8 else 0) | \
                       (_lib.MOE_ADAMW_PARAM_BF16 if p.dtype == _BF16 else 0)
+        _refuse_overlaps([("params", self.params)] + [("state[%r]" % (s,), self.state[s]) for s in self._names])
         self._table, self._cols, self._flags = table, cols, cols["flags"][:n].copy()
         # (kept, so that nothing else is given a replaced tensor's memory, and with it an
         # address that step() knows, before step() has looked)

@@ -160,6 +160,13 @@ class TrainStack:
     def _own_layers(self):
         if len({id(layer) for layer in self.layers}) != len(self.layers):
             raise ValueError("a layer stands in several places: its gradients have to be added first")
+        at = {}
+        for i, layer in enumerate(self.layers):
+            for name, _ in self._LAYER:
+                w = getattr(layer, name)
+                if w.numel() and at.setdefault(w.data_ptr(), i) != i:
+                    raise ValueError("%s of layer %d is layer %d's: its gradients have to be added first" %
+                                     (name, i, at[w.data_ptr()]))
         return self.layers
 
     def parameters(self) -> list:
