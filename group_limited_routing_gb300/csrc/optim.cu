@@ -635,9 +635,26 @@ __global__ void __launch_bounds__(ADAM_THREADS, S8 ? 6 : 4) adamw_kernel(const _
     }
 }
 
+// Squares of a thread's elements, V at a time, in 64 bits: those that fp32 cannot hold.
+template <int V, bool BF16>
+__device__ __noinline__ double squares_64(const void *g, int n)
+{
+    double sum = 0.0;
+    for (int i = threadIdx.x * V; i < n; i += 256 * V)
+        for (int j = 0; j < V; ++j) {
+            const float x = BF16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(g)[i + j] << 16)
+                                 : static_cast<const float *>(g)[i + j];
+            if (x != 0.0f)
+                sum = fma((double)x, (double)x, sum);
+        }
+    return sum;
+}
+
 // Sum of squares of every tensor: a thread adds at most 32 squares in fp32
 // before they join a 64-bit sum, so the norm is as exact over 10^9 elements as over
-// a few; the blocks' sums are added in a fixed order.
+// a few; the blocks' sums are added in a fixed order.  Where the 32 overflow, or
+// their sum is so small that some may have vanished (`any`: bits of those that are not
+// zero), the thread takes them again in 64 bits.
 __global__ void __launch_bounds__(256) grad_norm_kernel(const __grid_constant__ NormTable tab, double *__restrict__ partial)
 {
     pdl_wait();
@@ -657,9 +674,11 @@ __global__ void __launch_bounds__(256) grad_norm_kernel(const __grid_constant__ 
         const long long i0 = (long long)(u - t.unit0) * NORM_UNIT;
         const long long n = min(t.n - i0, (long long)NORM_UNIT);
         float acc[4] = {};
+        uint32_t any = 0;
+        const bool whole = t.aligned && n == NORM_UNIT;
         if (t.bf16) {
             const uint16_t *g = static_cast<const uint16_t *>(t.g) + i0;
-            if (t.aligned && n == NORM_UNIT) {
+            if (whole) {
                 uint4 v[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -671,30 +690,44 @@ __global__ void __launch_bounds__(256) grad_norm_kernel(const __grid_constant__ 
                     for (int j = 0; j < 4; ++j) {
                         const float a = __uint_as_float(x[j] << 16), b = __uint_as_float(x[j] & 0xffff0000u);
                         acc[q] = fmaf(b, b, fmaf(a, a, acc[q]));
+                        any |= x[j] & 0x7fff7fffu;
                     }
                 }
             } else {
                 for (int i = threadIdx.x; i < n; i += 256) {
                     const float a = __uint_as_float((uint32_t)g[i] << 16);
                     acc[0] = fmaf(a, a, acc[0]);
+                    any |= g[i] & 0x7fffu;
                 }
             }
         } else {
             const float *g = static_cast<const float *>(t.g) + i0;
-            if (t.aligned && n == NORM_UNIT) {
+            if (whole) {
                 float4 v[8];
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
                     v[q] = __ldcs(reinterpret_cast<const float4 *>(g) + threadIdx.x + 256 * q);
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
+                for (int q = 0; q < 8; ++q) {
                     acc[q & 3] += fmaf(v[q].x, v[q].x, v[q].y * v[q].y) + fmaf(v[q].z, v[q].z, v[q].w * v[q].w);
+                    any |= __float_as_uint(v[q].x) | __float_as_uint(v[q].y) | __float_as_uint(v[q].z) | __float_as_uint(v[q].w);
+                }
             } else {
-                for (int i = threadIdx.x; i < n; i += 256)
+                for (int i = threadIdx.x; i < n; i += 256) {
                     acc[0] = fmaf(g[i], g[i], acc[0]);
+                    any |= __float_as_uint(g[i]);
+                }
             }
+            any &= 0x7fffffffu;
         }
-        sum += (double)acc[0] + (double)acc[1] + ((double)acc[2] + (double)acc[3]);
+        const float all = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        double more = (double)acc[0] + (double)acc[1] + ((double)acc[2] + (double)acc[3]);
+        if (any && !(all >= 0x1p-90f && all < INFINITY)) {
+            const void *g = static_cast<const char *>(t.g) + i0 * (t.bf16 ? 2 : 4);
+            more = t.bf16 ? whole ? squares_64<8, true>(g, (int)n) : squares_64<1, true>(g, (int)n)
+                          : whole ? squares_64<4, false>(g, (int)n) : squares_64<1, false>(g, (int)n);
+        }
+        sum += more;
     }
 #pragma unroll
     for (int off = 16; off; off >>= 1)
@@ -731,7 +764,7 @@ __global__ void __launch_bounds__(256) grad_norm_finish_kernel(const double *__r
         t = sqrt(t);
         *norm = (float)t;
         if (scale) {
-            const bool finite = t <= 1.7976931348623157e308;
+            const bool finite = (float)t < INFINITY;
             *scale = !finite ? __uint_as_float(0x7fc00000u) : t > (double)max_norm ? (float)((double)max_norm / t) : 1.0f;
         }
     }

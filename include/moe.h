@@ -618,8 +618,8 @@ int moe_adamw(int32_t count, const moe_adamw_tensor *tensors, const moe_adamw_cf
 
 /* The 2-norm over `count` gradients (a HOST array; p and the states are not looked
  * at): norm [1] fp32, and scale [1] fp32 (or NULL) = max_norm / norm where that is
- * below 1, else 1, and NaN where the norm is not finite.  Squares are fp32, their
- * sums 64 bits.  Deterministic.  Workspace of
+ * below 1, else 1, and NaN where the norm is not finite.  Squares are fp32 (64 bits
+ * where fp32 cannot hold them), their sums 64 bits.  Deterministic.  Workspace of
  * moe_grad_norm_workspace_bytes(count) bytes. */
 size_t moe_grad_norm_workspace_bytes(int32_t count);
 int moe_grad_norm(int32_t count, const moe_adamw_tensor *tensors, float max_norm, float *norm, float *scale, void *ws,
