@@ -36,7 +36,7 @@ MOE_WS_BACKWARD = 2
 EXPORTS = ("moe_workspace_bytes", "moe_workspace_init", "moe_route", "moe_router_logits",
            "moe_route_from_logits", "moe_forward", "moe_get_status", "moe_last_launch_count",
            "moe_profile_enable", "moe_profile_read", "moe_kernel_name", "moe_strerror", "moe_route_static",
-           "moe_debug_inject_timeout", "moe_rmsnorm", "moe_expert_feedback", "moe_prepare_router",
+           "moe_debug_inject_timeout", "moe_debug_scaled_tile", "moe_rmsnorm", "moe_expert_feedback", "moe_prepare_router",
            "moe_route_prepared", "moe_dense_workspace_bytes", "moe_dense_ffn", "moe_backward",
            "moe_layer_workspace_bytes", "moe_layer", "moe_router_scores", "moe_ep_dispatch_workspace_bytes",
            "moe_ep_dispatch", "moe_expert_rows_workspace_bytes", "moe_expert_rows", "moe_combine",
@@ -146,6 +146,8 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.moe_rmsnorm.restype = ctypes.c_int
         lib.moe_debug_inject_timeout.argtypes = [ctypes.c_int]
         lib.moe_debug_inject_timeout.restype = ctypes.c_int
+        lib.moe_debug_scaled_tile.argtypes = [I32, I32, I32, ctypes.c_int64, I32, I32, I32, P, P]
+        lib.moe_debug_scaled_tile.restype = ctypes.c_int
         lib.moe_route_static.argtypes = [C, P, P, P, P, P, P, P, P, P, P]
         lib.moe_route_static.restype = ctypes.c_int
         lib.moe_ep_dispatch_workspace_bytes.argtypes = [C, I32]

@@ -485,6 +485,20 @@ int moe_scaled_weight_gradient(int32_t M, int32_t N, int64_t P, int32_t E, int32
     return rc;
 }
 
+int moe_debug_scaled_tile(int32_t weight_gradient, int32_t M, int32_t N, int64_t K, int32_t E, int32_t out_f32,
+                          int32_t sms, int32_t *rows, int32_t *columns)
+{
+    const int rc = check_product(M, N, K, E, 0, 0, out_f32);
+    if (rc != MOE_OK)
+        return rc;
+    if (M < 1 || K < 1 || sms < 2 || !rows || !columns)
+        return MOE_ERR_INVALID_ARG;
+    const ScaledTile t = scaled_tile(weight_gradient ? SM_SUM : E > 0 ? SM_ROWS : SM_DENSE, M, N, E, ceil_div(K, 128), out_f32 != 0, sms);
+    *rows = t.pair ? 256 : 128;
+    *columns = t.columns;
+    return MOE_OK;
+}
+
 int moe_adamw(int32_t count, const moe_adamw_tensor *tensors, const moe_adamw_cfg *cfg, const float *grad_scale,
               const int64_t *step_on_device, const float *lr_on_device, void *stream)
 {

@@ -672,6 +672,12 @@ const char *moe_kernel_name(int kernel_id);
  * is then meaningless, but the CUDA context stays usable.  0 cancels. */
 int moe_debug_inject_timeout(int launches);
 
+/* For tests: the tile that moe_scaled_product (weight_gradient = 0) or
+ * moe_scaled_weight_gradient (1, K its P) takes for these sizes on a GPU of `sms` SMs:
+ * *rows 256 (a pair of CTAs) or 128 (one) and *columns of the output.  No CUDA call. */
+int moe_debug_scaled_tile(int32_t weight_gradient, int32_t M, int32_t N, int64_t K, int32_t E, int32_t out_f32,
+                          int32_t sms, int32_t *rows, int32_t *columns);
+
 /* Static description of a return code. */
 const char *moe_strerror(int code);
 
