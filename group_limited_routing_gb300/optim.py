@@ -56,11 +56,11 @@ _shape = operator.attrgetter("shape")
 def _refuse_overlaps(named) -> None:
     """Lists of (name, contiguous tensors or Nones) of which no two may share memory: the
     kernel's blocks read and write all of them at once."""
-    spans = sorted((t.data_ptr(), t.numel() * t.element_size(), "%s[%d]" % (name, i)) for name, held in named
+    spans = sorted((t.data_ptr(), t.numel() * t.element_size(), name, i) for name, held in named
                    for i, t in enumerate(held) if t is not None and t.numel())
-    for (a, size, first), (b, _, second) in zip(spans, spans[1:]):
+    for (a, size, *first), (b, _, *second) in zip(spans, spans[1:]):
         if a + size > b:
-            raise ValueError("%s and %s overlap" % (first, second))
+            raise ValueError("%s[%d] and %s[%d] overlap" % (*first, *second))
 
 
 def _addresses_of(tensors) -> list:
