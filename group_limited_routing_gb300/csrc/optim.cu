@@ -19,8 +19,9 @@
 // same reason.  The random bits are a hash of the element's index, the tensor's
 // ordinal, the step and a seed, so a step is reproducible.
 //
-// The step is bound by memory: per element the parameter, the gradient and the
-// states, read and written once.  A warp takes 512 elements of one tensor, all
+// With fp32 states the step is bound by memory: per element the parameter, the gradient
+// and the states, read and written once; with 8-bit states by the instructions an element
+// takes (adamw_kernel).  A warp takes 512 elements of one tensor, all
 // of whose loads it issues before the first is used.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -568,10 +569,14 @@ __device__ __forceinline__ void step_any(const AdamTensor &t, const Step &c, lon
 }
 
 // A kernel for each kind of state.  Blocks of 128 threads.  With 8-bit states 2^26
-// elements take 155 us with 6 blocks to an SM, 169 with 4, 161 with 5; blocks of 1024
-// elements 162 to 173, a block that loops over four times the elements 344; four
-// elements to a lane instead of eight 158.  With fp32 states (286 us with a master
-// copy) 3 to 6 blocks make no difference: memory bounds them.
+// elements take 176 us with 6 blocks to an SM, of which 21 are for rounding every
+// operation as the formula does (155 with an approximate root and reciprocal; with the
+// compiler's root and quotient in their place 190).  Counters: 85 instructions an element,
+// issue slots 81% used, and the pipe of paired fp32 and integer products nearly as much.
+// Before those 21: 169 with 4 blocks, 161 with 5; blocks of 1024 elements 162 to 173, a
+// block that loops over four times the elements 344; four elements to a lane instead of
+// eight 158.  With fp32 states (286 us with a master copy) 3 to 6 blocks make no
+// difference: memory bounds them, and rounding costs nothing.
 template <int N, bool S8>
 __global__ void __launch_bounds__(ADAM_THREADS, S8 ? 6 : 4) adamw_kernel(const __grid_constant__ AdamTable<N> tab)
 {

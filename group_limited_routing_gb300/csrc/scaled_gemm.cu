@@ -23,8 +23,8 @@
 // The scales have rings of their own in shared memory and in TMEM, four blocks to a
 // slot, and run well ahead of the operands: a write to TMEM and its handshake take
 // more than a thousand cycles while MMAs run, an operand stage's MMAs 550.  With words of
-// four equal bytes, one for each stage, a pair reached 1260 TFLOP/s (8192 x 8192 x
-// 8192) in one ring with the operands and 3010 with two groups of warps taking turns.
+// four equal bytes, one for each stage, in the operands' ring a pair reached 2910 TFLOP/s
+// (8192 x 8192 x 8192), with words of four blocks on this ring 3020, all else alike.
 //
 // The tensor core cuts its running sum to fp32 instead of rounding it, so it drifts
 // towards zero as it grows: by 4e-6 over 8192 of K of one sign, 2.4e-5 over 32768.
@@ -396,8 +396,8 @@ __global__ void __launch_bounds__(SgCfg<BN, PAIR, F32>::THREADS) scaled_gemm_ker
     auto acc_col = [&](uint32_t i) { return tmem + (i & 1u) * C::SLOT_STEP; };
     // An arrival at a barrier of the even CTA.  It hands over TMEM, whose accesses have
     // completed before it (wait::st, wait::ld), and no memory, so it needs no release
-    // at cluster scope: with one, which waits some 2000 cycles, a pair reached 1900
-    // TFLOP/s (8192 x 8192 x 8192) instead of 2910.
+    // at cluster scope.  With one: 8192 x 8192 x 8192 2990 TFLOP/s instead of 3400, 65536 x
+    // 2048 x 1024 1840 instead of 2520.
     auto arrive_leader = [&](uint32_t bar) {
         if (PAIR)
             asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(bar, 0)) : "memory");

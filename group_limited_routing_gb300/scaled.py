@@ -200,8 +200,8 @@ def product(a: Scaled, b: Scaled, *, offsets=None, dtype=torch.bfloat16, ws: Opt
 
 def weight_gradient(dy_t: Scaled, x_t: Scaled, *, dtype=torch.float32, ws: Optional[SizedWorkspace] = None, out=None):
     """moe_scaled_weight_gradient: d_y^T x of quantize_columns(d_y) [N, P] and
-    quantize_columns(x) [K, P]: [N, K], or with grouped columns [E, N, K], zeros for a
-    group without rows."""
+    quantize_columns(x) [K, P]: [N, K], or with grouped columns (both of the same
+    offsets, which is not looked at) [E, N, K], zeros for a group without rows."""
     fa, pa, psa = _checked(dy_t, "dy_t", 2)
     fb, pb, psb = _checked(x_t, "x_t", 2)
     dev = dy_t[0].device

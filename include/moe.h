@@ -539,7 +539,8 @@ int moe_unsort_rows_backward(int32_t T, int32_t k, int32_t H, int32_t f32, int64
  * starts a block of the transpose and ends with zeros up to a whole block; starts
  * [E + 1] int32 out: blocks of the groups before each; P a multiple of 128, at
  * least 128 (floor(R / 128) + E), E <= 1024.  Rows that belong to no group are left out of both.
- * Both forms are made from one read. */
+ * Both forms are made from one read.  K <= 2^24; R and P at most 65535 blocks of 128,
+ * batch at most 65535. */
 int moe_scaled_quantize(int32_t batch, int32_t R, int32_t K, int32_t f32, int32_t e_five_m_two, const void *x,
                         uint8_t *q, uint8_t *scale, uint8_t *qt, uint8_t *scale_t, int32_t E, const int32_t *offsets,
                         int32_t *starts, int64_t P, void *stream);
@@ -555,7 +556,9 @@ int moe_scaled_quantize_rows(int32_t T, int32_t k, int32_t K, int32_t f32, int32
  * ceil(K / 128), ld]) and rows offsets[e] to offsets[e + 1] - 1 of A are
  * multiplied with B[e]; rows of no group stay as they were.  The scaled products
  * are summed in fp32 by the tensor cores (with an fp32 output in parts of 2048, which
- * are added in fp32) and rounded once.  Workspace of
+ * are added in fp32) and rounded once.  The tensor core cuts its sum every 32 of K, by
+ * less than 2^-23 of it: over a K of one sign a bf16 output's sum, which has no parts, is
+ * 2.4e-5 too small at 32768, against its rounding of 2^-9.  Workspace of
  * MOE_SCALED_WS_BYTES for the status word. */
 #define MOE_SCALED_WS_BYTES 256
 int moe_scaled_product(int32_t M, int32_t N, int32_t K, int32_t E, int32_t a_format, int32_t b_format, int32_t out_f32,
@@ -565,7 +568,9 @@ int moe_scaled_product(int32_t M, int32_t N, int32_t K, int32_t E, int32_t a_for
 /* The gradient of a weight, from the transposed forms of the output's gradient
  * (A [M, P]) and of the input (B [N, P]):
  *   out [E, M, N], out[e] = sum over blocks starts[e] to starts[e + 1] - 1 of P of A B^T
- * (zeros for a group without blocks), bf16 or fp32, N % 8 == 0, P % 128 == 0.
+ * (zeros for a group without blocks), bf16 or fp32, N % 8 == 0, P % 128 == 0.  Both
+ * operands have to be of the same offsets, so that starts holds for both (that is not
+ * looked at: others give the sum of unrelated rows).
  * E = 0: one sum over all of P (P % 16 == 0), out [M, N]. */
 int moe_scaled_weight_gradient(int32_t M, int32_t N, int64_t P, int32_t E, int32_t a_format, int32_t b_format,
                                int32_t out_f32, const uint8_t *A, const uint8_t *A_scale, const uint8_t *B,
@@ -590,8 +595,8 @@ int moe_scaled_weight_gradient(int32_t M, int32_t N, int64_t P, int32_t E, int32
  * The random bits are a function of seed, step, ordinal and the element's index.
  * grad_scale [1] fp32 on the device or NULL: g is multiplied by it first (the
  * result of moe_grad_norm); if it is not finite, nothing is written.
- * step_on_device [1] int64 and lr_on_device [1] fp32 take the place of cfg's step
- * and lr where they are not NULL (a captured step reads them anew).
+ * step_on_device [1] int64, at least 1, and lr_on_device [1] fp32 take the place of
+ * cfg's step and lr where they are not NULL (a captured step reads them anew).
  * No two tensors may overlap.  Elements of any alignment of their type; n <= 2^40. */
 #define MOE_ADAMW_STATES_IN_BYTES 1
 #define MOE_ADAMW_PARAM_BF16 2
