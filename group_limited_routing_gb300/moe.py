@@ -716,7 +716,8 @@ def sort_tokens(topk_idx, E: int, *, ws: Optional[SizedWorkspace] = None, out=No
     stable sort of the (token, j) pairs of topk_idx [T, k] int32 by expert: expert
     e has rows offsets[e] to offsets[e + 1] - 1, pair (t, j) row slot_of[t, j] (-1
     where topk_idx is -1: dropped).  `out` = (offsets, slot_of) is filled instead of
-    allocating."""
+    allocating.  Ids that name no expert are dropped and noted in the workspace's
+    status, which only a `ws` that is given lets its caller read."""
     T, k = _matrix(topk_idx, "topk_idx")
     dev = topk_idx.device
     i32 = torch.int32

@@ -49,7 +49,8 @@ class Scaled(NamedTuple):
 
 
 def workspace(device=None) -> SizedWorkspace:
-    """The workspace of product and weight_gradient (their status word)."""
+    """The workspace of product and weight_gradient: their status word (a time-out), which
+    without a workspace of the caller's goes with a temporary one."""
     return SizedWorkspace(_lib.MOE_SCALED_WS_BYTES, "moe_scaled_product", device)
 
 
